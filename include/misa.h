@@ -20,6 +20,16 @@
  *                   of MISA and the token axis of HISA combined.
  *   misa_block_means  the query-independent block means the router pools.
  *
+ * Around the selection it keeps the caches that it and its consumer read, and
+ * computes the attention that consumes it:
+ *
+ *   misa_cache_write, misa_cache_read  rows of indexer keys or of latents,
+ *                   coded as they are written, and read back.
+ *   misa_latent_attention    attention over one shared latent vector a token
+ *                   (absorbed form), on the selected or on all visible keys.
+ *   misa_expanded_attention  the same attention over per-head keys and values
+ *                   expanded from the latents.
+ *
  * Definitions (the pages give the structure; the exact formulas are fixed here):
  *   z(t,h,s)  = q[t,h,:] . k[s,:]
  *   I_S(t,s)  = sum_{h in S} w[t,h] * max(0, z(t,h,s))        (no renormalisation)
@@ -240,6 +250,109 @@ misa_status hisa_maxpool_topk(const misa_problem* p, int32_t m, int32_t k, int32
  * for misa_score_topk and hisa_topk. */
 misa_status misa_hisa_topk(const misa_problem* p, int32_t A, const int32_t* heads, int32_t m, int32_t k,
                            int32_t* idx, float* scores, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ caches
+ *
+ * A cache holds `rows` rows of d coded columns and dr rotary columns:
+ *   indexer keys  d = 128, dr = 0   (misa_problem.K and k_scale read them)
+ *   latents       d = 512, dr = 64  (misa_latent_attention reads them)
+ * (d = 128 or 512 with dr = 0 or 64 are supported). dtype MISA_K_BF16: c is
+ * [rows, d + dr] bf16 bits, scale and rope are NULL. dtype MISA_K_FP8_E4M3FN:
+ * c is [rows, d] E4M3FN codes with value = code * scale[row], and rope is
+ * [rows, dr] bf16 bits (NULL iff dr == 0). c and rope are 16-byte aligned. */
+typedef struct misa_cache {
+  int32_t rows;
+  int32_t d;
+  int32_t dr;
+  int32_t dtype;  /* misa_kdtype */
+  void* c;
+  float* scale;
+  void* rope;
+} misa_cache;
+
+/* Writes row i of x [n, d + dr] (bf16 bits) to row slots[i] of the cache, for
+ * every i with 0 <= slots[i] < rows; other entries write nothing, and rows of
+ * the cache that no slot names stay as they are. bf16 rows are copied. Coded
+ * rows: with a = max |x[i, 0:d]|, scale = 2^e for the smallest e >= -126 with
+ * a <= 448 * 2^e (1 if a == 0), code = x / scale rounded to nearest even; the
+ * rotary columns are copied. A power-of-two scale leaves one rounding per
+ * value, and code * scale is exact in bf16. A row with an infinity or NaN among
+ * its d columns gets scale NaN and NaN codes. Slots >= 0 must be distinct:
+ * a row named twice holds either row's values, possibly mixed. n == 0 is a no-op. */
+misa_status misa_cache_write(const misa_cache* cache, const void* x, int32_t n, const int32_t* slots, void* stream);
+
+/* Reads row slots[i] of the cache into row i of out [n, d + dr] (bf16 bits):
+ * code * scale formed in fp32 and rounded to bf16 (exact for the scales that
+ * misa_cache_write writes); rotary columns and bf16 rows are copied. A slot
+ * outside [0, rows) gives a row of zeros; a slot may occur more than once. */
+misa_status misa_cache_read(const misa_cache* cache, const int32_t* slots, int32_t n, void* out, void* stream);
+
+/* --------------------------------------------------------- latent attention
+ *
+ * Absorbed form: the cache row of a token holds its latent vector c (512) and
+ * its rotary key (64), shared by all heads; q[t,h] holds the head's query taken
+ * into the latent space (512) and its rotary part (64):
+ *   S(t,h,s)  = sm_scale * (q[t,h,0:512] . c[s] + q[t,h,512:576] . rope[s])
+ *   out[t,h]  = sum_s p(t,h,s) c[s],  p = softmax of S over the query's keys
+ *   lse[t,h]  = log sum_s exp S(t,h,s)
+ * The query's keys are, with b = base[t] (0 if base is NULL) the cache row where
+ * its sequence begins,
+ *   idx given:  rows b + idx[t,j], j < k, for idx[t,j] >= 0 (as the selection
+ *               entry points write them: -1 is padding; an index that occurs
+ *               twice counts twice; order does not matter). pos must be NULL.
+ *   idx NULL:   rows b .. b + pos[t]; k must be 0.
+ * Rows outside [0, rows) of the cache are no keys, and base[t] < 0 leaves no
+ * key; what a row holds that is not a key of a query (infinities and NaN too)
+ * has no effect on that query. A query without keys gets out = 0
+ * and lse = -inf. Scores, weights' totals and sums are held in fp32; a weight is
+ * rounded to bf16 for its product with the values. Results do not depend on
+ * what else runs; the same call gives the same bits. */
+typedef struct misa_latent_problem {
+  int32_t T;              /* queries (T == 0 is a no-op) */
+  int32_t H;              /* heads per query, >= 1 */
+  int32_t k;              /* entries of a query's list (idx), or 0 */
+  float sm_scale;         /* softmax scale, finite */
+  const void* q;          /* [T,H,576] bf16 bits, 16-byte aligned */
+  const int32_t* idx;     /* [T,k] or NULL */
+  const int32_t* pos;     /* [T], required iff idx is NULL */
+  const int32_t* base;    /* [T] or NULL */
+  misa_cache cache;       /* d = 512, dr = 64 */
+} misa_latent_problem;
+
+/* Bytes of workspace a call needs (0 for an invalid request; at least 256).
+ * q, pos and base's contents do not matter, but whether idx and base are NULL does. */
+size_t misa_latent_workspace_bytes(const misa_latent_problem* p);
+
+/* out [T,H,512] bf16 bits (16-byte aligned); lse [T,H] float32 or NULL. */
+misa_status misa_latent_attention(const misa_latent_problem* p, void* out, float* lse, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Expanded form, for prompts: every head has its own key (128 values, then the
+ * rotary key shared by the heads) and value (128):
+ *   S(t,h,s)  = sm_scale * (q[t,h,0:128] . kv[s,h,0:128] + q[t,h,128:192] . rope[s])
+ *   out[t,h]  = sum_s p(t,h,s) kv[s,h,128:256]
+ * over the keys b .. b + pos[t] of query t that lie in [0, L), b = base[t] (0 if
+ * base is NULL; b < 0 leaves no key): packed sequences have their own base each, pos < 0 marks a
+ * padded row. Queries may come in any order; neighbours with overlapping keys
+ * run fastest. Otherwise as misa_latent_attention. */
+typedef struct misa_expanded_problem {
+  int32_t T;
+  int32_t H;
+  int32_t L;              /* keys, >= 1 */
+  float sm_scale;
+  const void* q;          /* [T,H,192] bf16 bits */
+  const void* kv;         /* [L,H,256] bf16 bits: key (without rotary part), value */
+  const void* rope;       /* [L,64] bf16 bits, rows rope_ld elements apart */
+  int64_t rope_ld;        /* >= 64, a multiple of 8 */
+  const int32_t* pos;     /* [T] */
+  const int32_t* base;    /* [T] or NULL */
+} misa_expanded_problem;
+
+size_t misa_expanded_workspace_bytes(const misa_expanded_problem* p);
+
+/* out [T,H,128] bf16 bits (16-byte aligned); lse [T,H] float32 or NULL. */
+misa_status misa_expanded_attention(const misa_expanded_problem* p, void* out, float* lse, void* ws, size_t ws_bytes,
+                                    void* stream);
 
 /* Short static text for a status code. */
 const char* misa_status_str(int32_t status);

@@ -15,10 +15,17 @@ Entry points (same names as the C ABI in include/misa.h):
     hisa_topk(q, w, K, pos, B, m, k, k_scale=None)      -> (idx, scores)
     hisa_block_scores(q, w, K, pos, B, k_scale=None)    -> beta [T, ceil(L/B)] f32
     misa_hisa_topk(q, w, K, pos, B, A, m, k, k_scale=None, heads=None) -> (idx, scores)
+    cache_write(x, slots, C, c_scale=None, rope=None)   -> None (rows slots of the cache are written)
+    cache_read(slots, C, c_scale=None, rope=None)       -> rows [n, d (+ 64)] bf16
+    latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None,
+                     with_lse=False)                    -> out [T, H, 512] bf16 (, lse [T, H] f32)
+    expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False)
+                                                        -> out [T, H, 128] bf16 (, lse [T, H] f32)
 
-Inputs are CUDA (HIP) tensors: q [T,H,128] bfloat16 (or int16 bf16 bits),
+Inputs of the selection are CUDA (HIP) tensors: q [T,H,128] bfloat16 (or int16 bf16 bits),
 w [T,H] float32, K [L,128] bfloat16 / int16 bits, or uint8 / float8_e4m3fn
-codes with k_scale [L] float32, pos [T] int32.
+codes with k_scale [L] float32, pos [T] int32. Caches and attention take
+bfloat16 and E4M3FN tensors of the widths that include/misa.h lists.
 """
 from __future__ import annotations
 
@@ -53,6 +60,23 @@ class Problem(ctypes.Structure):
                 ("q_dtype", ctypes.c_int32), ("q_scale", ctypes.c_void_p)]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("d", ctypes.c_int32), ("dr", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("c", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rope", ctypes.c_void_p)]
+
+
+class LatentProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("k", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("base", ctypes.c_void_p), ("cache", Cache)]
+
+
+class ExpandedProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("L", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("kv", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("rope_ld", ctypes.c_int64), ("pos", ctypes.c_void_p), ("base", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -78,6 +102,12 @@ def lib() -> ctypes.CDLL:
             "hisa_maxpool_topk": (i32, [P, i32, i32, vp, vp, vp, sz, vp]),
             "hisa_block_scores": (i32, [P, vp, ctypes.c_int64, vp, sz, vp]),
             "misa_hisa_topk": (i32, [P, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
+            "misa_cache_write": (i32, [ctypes.POINTER(Cache), vp, i32, vp, vp]),
+            "misa_cache_read": (i32, [ctypes.POINTER(Cache), vp, i32, vp, vp]),
+            "misa_latent_workspace_bytes": (sz, [ctypes.POINTER(LatentProblem)]),
+            "misa_latent_attention": (i32, [ctypes.POINTER(LatentProblem), vp, vp, vp, sz, vp]),
+            "misa_expanded_workspace_bytes": (sz, [ctypes.POINTER(ExpandedProblem)]),
+            "misa_expanded_attention": (i32, [ctypes.POINTER(ExpandedProblem), vp, vp, vp, sz, vp]),
             "misa_status_str": (ctypes.c_char_p, [i32]),
             "misa_last_error": (ctypes.c_char_p, []),
             "misa_profile_enable": (i32, [i32]),
@@ -297,6 +327,147 @@ def misa_hisa_topk(q, w, K, pos, B, A, m, k, k_scale=None, heads=None, ws=None, 
     _check(lib().misa_hisa_topk(ctypes.byref(p), A, _ptr(heads), m, k, _ptr(idx), _ptr(sc), _ptr(ws), n,
                                 _stream()))
     return idx, sc
+
+
+# ---------------------------------------------------------------- caches and latent attention
+
+LATENT, ROTARY, NOPE, VALUE = 512, 64, 128, 128
+
+
+def _tensor(t: Optional[torch.Tensor], name: str, dtypes, shape, device=None):
+    """Checks one argument: a contiguous GPU tensor of one of `dtypes` and of
+    `shape` (None: any size), on `device` when one is given."""
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    _dev(t, name)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != len(shape) or any(want is not None and want != n for want, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {['any' if n is None else n for n in shape]}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+_BF16, _CODES = (torch.bfloat16, torch.int16), (torch.uint8, torch.float8_e4m3fn)
+
+
+def make_cache(C: torch.Tensor, c_scale: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None) -> Cache:
+    """Fill the C cache struct from tensors (no copies): C [rows, d + dr] bfloat16,
+    or E4M3FN codes [rows, d] with c_scale [rows] float32 and, for rows with
+    rotary columns, rope [rows, 64] bfloat16."""
+    _tensor(C, "C", _BF16 + _CODES, (None, None))
+    rows, width = C.shape
+    if C.dtype in _CODES:
+        _tensor(c_scale, "c_scale", (torch.float32,), (rows,), C.device)
+        if rope is not None:
+            _tensor(rope, "rope", _BF16, (rows, ROTARY), C.device)
+        return Cache(rows, width, 0 if rope is None else ROTARY, KDT_FP8, _ptr(C), _ptr(c_scale), _ptr(rope))
+    if c_scale is not None or rope is not None:
+        raise ValueError("c_scale and rope are only for E4M3FN codes (bf16 rows hold their rotary values)")
+    dr = ROTARY if width in (128 + ROTARY, LATENT + ROTARY) else 0
+    return Cache(rows, width - dr, dr, KDT_BF16, _ptr(C), None, None)
+
+
+def cache_write(x, slots, C, c_scale=None, rope=None):
+    """Write row i of x [n, d (+ 64)] bfloat16 to row slots[i] (int32) of the
+    cache, coded if C holds codes; slots outside the cache write nothing. Slots
+    inside it must be distinct."""
+    c = make_cache(C, c_scale, rope)
+    _tensor(x, "x", _BF16, (None, c.d + c.dr), C.device)
+    _tensor(slots, "slots", (torch.int32,), (x.shape[0],), C.device)
+    with torch.cuda.device(C.device):
+        _check(lib().misa_cache_write(ctypes.byref(c), _ptr(x), x.shape[0], _ptr(slots), _stream()))
+
+
+def cache_read(slots, C, c_scale=None, rope=None, out=None):
+    """Rows slots (int32 [n]) of the cache as bfloat16 [n, d (+ 64)]; a slot
+    outside the cache gives zeros."""
+    c = make_cache(C, c_scale, rope)
+    _tensor(slots, "slots", (torch.int32,), (None,), C.device)
+    n = slots.shape[0]
+    with torch.cuda.device(C.device):
+        if out is None:
+            out = torch.empty((n, c.d + c.dr), dtype=torch.bfloat16, device=C.device)
+        else:
+            _tensor(out, "out", _BF16, (n, c.d + c.dr), C.device)
+        _check(lib().misa_cache_read(ctypes.byref(c), _ptr(slots), n, _ptr(out), _stream()))
+    return out
+
+
+def _attention(call, need, p, q, width, with_lse, ws, out):
+    """Output, log-sums and workspace of an attention call, and the call."""
+    T, H, _ = q.shape
+    with torch.cuda.device(q.device):
+        if out is None:
+            out = torch.empty((T, H, width), dtype=torch.bfloat16, device=q.device)
+        else:
+            _tensor(out, "out", _BF16, (T, H, width), q.device)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if with_lse else None
+        n = need(ctypes.byref(p))
+        if n == 0:  # the call itself reports what is wrong
+            _check(call(ctypes.byref(p), _ptr(out), _ptr(lse), None, 0, _stream()))
+        if ws is None or ws.numel() * ws.element_size() < n:
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:
+            _dev(ws, "ws")
+            if ws.device != q.device:
+                raise ValueError(f"ws is on {ws.device}, not on {q.device}")
+        _check(call(ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), n, _stream()))
+    return (out, lse) if with_lse else out
+
+
+def make_latent_problem(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None) -> LatentProblem:
+    c = make_cache(C, c_scale, rope)
+    _tensor(q, "q", _BF16, (None, None, LATENT + ROTARY), C.device)
+    T, H, _ = q.shape
+    if (pos is None) == (idx is None):
+        raise ValueError("give either pos [T] (every visible key) or idx [T, k] (the keys of a list)")
+    if pos is not None:
+        _tensor(pos, "pos", (torch.int32,), (T,), q.device)
+    else:
+        _tensor(idx, "idx", (torch.int32,), (T, None), q.device)
+        if idx.shape[1] < 1:
+            raise ValueError("idx must have at least one column")
+    if base is not None:
+        _tensor(base, "base", (torch.int32,), (T,), q.device)
+    return LatentProblem(T, H, 0 if idx is None else idx.shape[1], float(sm_scale), _ptr(q), _ptr(idx), _ptr(pos),
+                         _ptr(base), c)
+
+
+def latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None, with_lse=False,
+                     ws=None, out=None):
+    """Attention of q [T, H, 576] over latent cache rows (absorbed form): the
+    keys idx [T, k] int32 as the selections return them (-1: none), or every
+    key up to pos [T] int32; base [T] int32 is the cache row where each query's
+    sequence begins. C, c_scale, rope: see make_cache (d = 512, rotary 64)."""
+    p = make_latent_problem(q, C, sm_scale, pos, idx, c_scale, rope, base)
+    return _attention(lib().misa_latent_attention, lib().misa_latent_workspace_bytes, p, q, LATENT, with_lse, ws, out)
+
+
+def make_expanded_problem(q, kv, rope, pos, sm_scale, base=None) -> ExpandedProblem:
+    _tensor(q, "q", _BF16, (None, None, NOPE + ROTARY))
+    T, H, _ = q.shape
+    _tensor(kv, "kv", _BF16, (None, H, NOPE + VALUE), q.device)
+    L = kv.shape[0]
+    if not rope.is_cuda or rope.dtype not in _BF16 or tuple(rope.shape) != (L, ROTARY) or rope.device != q.device:
+        raise ValueError("rope must be a bfloat16 GPU tensor [L, 64] on q's device")
+    if rope.stride(1) != 1 or (L > 1 and rope.stride(0) < ROTARY):
+        raise ValueError("rope's rows must be contiguous")
+    _tensor(pos, "pos", (torch.int32,), (T,), q.device)
+    if base is not None:
+        _tensor(base, "base", (torch.int32,), (T,), q.device)
+    ld = rope.stride(0) if L > 1 else ROTARY
+    return ExpandedProblem(T, H, L, float(sm_scale), _ptr(q), _ptr(kv), _ptr(rope), ld, _ptr(pos), _ptr(base))
+
+
+def expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False, ws=None, out=None):
+    """Attention of q [T, H, 192] over per-head keys and values kv [L, H, 128 +
+    128] with rotary keys rope [L, 64] (rows may be strided, as the last columns
+    of read cache rows are): keys base[t] .. base[t] + pos[t] of query t."""
+    p = make_expanded_problem(q, kv, rope, pos, sm_scale, base)
+    return _attention(lib().misa_expanded_attention, lib().misa_expanded_workspace_bytes, p, q, VALUE, with_lse, ws,
+                      out)
 
 
 def profile_enable(on: bool = True):

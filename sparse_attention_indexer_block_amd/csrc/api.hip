@@ -12,6 +12,7 @@
 
 #include "../../include/misa.h"
 #include "launch.h"
+#include "status.h"
 
 namespace misa {
 
@@ -19,7 +20,7 @@ namespace misa {
 
 static thread_local std::string g_last_error;
 
-static misa_status fail(misa_status st, const char* fmt, ...) {
+misa_status fail(misa_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -29,7 +30,7 @@ static misa_status fail(misa_status st, const char* fmt, ...) {
   return st;
 }
 
-static misa_status hip_fail(hipError_t e, const char* where) {
+misa_status hip_fail(hipError_t e, const char* where) {
   return fail(MISA_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
@@ -187,8 +188,6 @@ static Tp* at(void* ws, size_t off) {
 
 // ---------------------------------------------------------------- validation
 
-static bool aligned(const void* ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
-
 static misa_status check_problem(const misa_problem* p, bool need_queries) {
   if (!p) return fail(MISA_ERR_INVALID_ARG, "problem is NULL");
   if (p->T < 0) return fail(MISA_ERR_INVALID_ARG, "T = %d is negative", p->T);
@@ -237,18 +236,6 @@ static misa_status check_out(const void* ptr, const char* name) {
   if (!aligned(ptr, 4)) return fail(MISA_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
   return MISA_OK;
 }
-
-#define MISA_TRY(expr)                   \
-  do {                                   \
-    misa_status _st = (expr);            \
-    if (_st != MISA_OK) return _st;      \
-  } while (0)
-
-#define HIP_TRY(expr, where)                     \
-  do {                                           \
-    hipError_t _e = (expr);                      \
-    if (_e != hipSuccess) return hip_fail(_e, where); \
-  } while (0)
 
 // ---------------------------------------------------------------- pipelines
 
