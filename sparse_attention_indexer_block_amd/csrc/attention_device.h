@@ -37,6 +37,16 @@ __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
       : "s"(lds), "v"(src)
       : "memory");
 }
+// The same from base + off, base uniform over the wave.
+__device__ __forceinline__ void copy16_to_lds_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Workgroup barrier that waits for this wave's LDS accesses only (copies to
@@ -55,14 +65,50 @@ __device__ __forceinline__ uint32_t lds_addr(Tp* p) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
+// Values of lane l ^ 32 (and l ^ 16) exchanged in registers: with both operands
+// the same, the two results hold the lower and the upper halves (odd and even
+// rows of 16 lanes) for every lane.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 // Maximum / sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ float max_over_groups(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, kWave));
-  return fmaxf(v, __shfl_xor(v, 32, kWave));
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 __device__ __forceinline__ float sum_over_groups(float v) {
-  v += __shfl_xor(v, 16, kWave);
-  return v + __shfl_xor(v, 32, kWave);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// LDS reads at a byte address (and the transposing ones: 16 lanes read rows of
+// 16 values, a lane gets one value of each row).
+template <typename Tp>
+__device__ __forceinline__ Tp lds_read(uint32_t at) {
+  return *(const __attribute__((address_space(3))) Tp*)(uintptr_t)at;
+}
+__device__ __forceinline__ s16x4 lds_read_tr16(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at);
+}
+__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)at));
+}
+__device__ __forceinline__ bf16x8 join_rows(s16x4 a, s16x4 b) {
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The softmax scale as the kernels use it: positive (queries change sign with
+// it) and not zero (the smallest scale weighs every key alike).
+__device__ __forceinline__ float scale_magnitude(float sm_log2) { return fmaxf(fabsf(sm_log2), 1e-37f); }
+__device__ __forceinline__ bf16x8 flip_sign(bf16x8 a, uint32_t mask) {
+  u32x4 v = __builtin_bit_cast(u32x4, a);
+  v ^= mask;
+  return __builtin_bit_cast(bf16x8, v);
 }
 
 // Eight E4M3FN codes -> eight bf16 values (exact).
@@ -77,6 +123,25 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(u32x2 v) {
 
 // Keys 0 .. pos of a prefix of `left` keys (0 for pos < 0).
 __device__ __forceinline__ int visible_keys(int pos, int left) { return pos < 0 ? 0 : (pos < left ? pos + 1 : left); }
+
+// A 32x32x16 product with its accumulator in vector registers, for a kernel whose
+// accumulation registers are all taken (the compiler's own choice is one kind
+// for a whole kernel). The compiler does not know that the asm is an MFMA, so
+// the waits it would insert stand here: two wait states after a vector
+// instruction that wrote an operand, none for the same accumulator, and
+// mfma_done() (16; 12 are required for this shape) before any other use of it.
+__device__ __forceinline__ void mfma_vgpr_first(f32x16& d, bf16x8 a, bf16x8 b) {
+  asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_vgpr(f32x16& d, bf16x8 a, bf16x8 b) {
+  asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_done(f32x16& d) { asm volatile("s_nop 15" : "+v"(d)); }
+
+// Keeps an accumulator in the accumulation registers on both sides of this
+// point: at the entry of a rare branch that changes it, the copies that the
+// change needs stay in the branch.
+__device__ __forceinline__ void in_agprs(f32x16& d) { asm volatile("" : "+a"(d)); }
 
 // A tile whose keys are not the same for all rows of a wave: a value that is
 // not finite must reach the rows that see its key and no other, but weight 0

@@ -103,11 +103,13 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   if (tile0 < tile1) stage(0, tile0);
 
   // Q as the B operand: K step ks, lane (query c, half h2): values 16 ks + 8 h2 .. + 7
+  const float sm = scale_magnitude(p.sm_log2);
   bf16x8 qf[12];
   {
+    const uint32_t sign = p.sm_log2 < 0.f ? 0x80008000u : 0u;
     const uint16_t* qr = p.q + ((int64_t)min(t, p.T - 1) * p.H + head) * (kNope + kRotary) + 8 * h2;
 #pragma unroll
-    for (int ks = 0; ks < 12; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qr + 16 * ks);
+    for (int ks = 0; ks < 12; ++ks) qf[ks] = flip_sign(*reinterpret_cast<const bf16x8*>(qr + 16 * ks), sign);
   }
   f32x16 o[4];
 #pragma unroll
@@ -118,8 +120,17 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   wait_copies();
   __syncthreads();
 
+  // The lane's addresses in a tile: its key row, its rotary row, and its row of
+  // the transposing reads (rows 16 j + 4 h2 + lo / 4 and eight further on). Every
+  // other chunk is an exclusive-or of the address, every other row an offset.
+  const uint32_t a_key = c * kKvRow + ((h2 ^ swz_kv(c)) * 16);
+  const uint32_t a_rot = kRope + c * (2 * kRotary) + ((h2 ^ swz_rot(c)) * 16);
+  const int vrow = 4 * h2 + (lo >> 2);
+  const uint32_t a_val =
+      vrow * kKvRow + (((kNope / 8 + 2 * ((lane >> 4) & 1) + ((lo & 3) >> 1)) ^ swz_kv(vrow)) * 16) + (lo & 1) * 8;
+
   for (int ti = tile0; ti < tile1; ++ti) {
-    const unsigned char* tb = tile[(ti - tile0) & 1];
+    const uint32_t tb = tile_lds + ((ti - tile0) & 1) * kTileBytes;
     if (ti + 1 < tile1) stage((ti + 1 - tile0) & 1, ti + 1);
     const int k0 = ti * kAttnTile;
     if (k0 < w_hi && k0 + kAttnTile > w_lo) {
@@ -129,74 +140,83 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
+      const uint32_t ka = tb + a_key, ra = tb + a_rot, va = tb + a_val;
 #pragma unroll
-      for (int ks = 0; ks < 12; ++ks)
+      for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int row = 32 * n + c;
-          const unsigned char* at = ks < 8 ? tb + row * kKvRow + (((2 * ks + h2) ^ swz_kv(row)) * 16)
-                                           : tb + kRope + row * (2 * kRotary) + (((2 * (ks - 8) + h2) ^ swz_rot(row)) * 16);
-          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(at), qf[ks], s[n], 0, 0, 0);
-        }
+        for (int n = 0; n < 2; ++n)
+          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lds_read<bf16x8>((ka ^ (32 * ks)) + n * 32 * kKvRow), qf[ks],
+                                                         s[n], 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lds_read<bf16x8>((ra ^ (32 * ks)) + n * 32 * 2 * kRotary),
+                                                         qf[8 + ks], s[n], 0, 0, 0);
+      // value operand of step (n, j): keys 32 n + 16 j .. + 15, values 32 d .. + 31
+      auto values = [&](int n, int j, int d) -> bf16x8 {
+        const uint32_t at = va ^ (64 * d) ^ (256 * j);
+        const int off = (32 * n + 16 * j) * kKvRow;
+        return join_rows(lds_read_tr16(at + off), lds_read_tr16((at ^ 32) + off + 8 * kKvRow));
+      };
       const bool mixed = k0 < f_lo || k0 + kAttnTile > f_hi;  // not every query sees every key
-      if (mixed) {
+      bool odd = false;                                       // and a value is not finite
+      if (__builtin_expect(mixed, 0)) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int key = k0 + 32 * n + 8 * (e >> 2) + 4 * h2 + (e & 3);
-            s[n][e] = key >= s_lo && key < s_hi ? s[n][e] * p.sm_log2 : -INFINITY;
+            s[n][e] = key >= s_lo && key < s_hi ? s[n][e] : -INFINITY;
           }
-      } else {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) s[n] *= p.sm_log2;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) odd |= any_odd(values(i >> 3, (i >> 2) & 1, i & 3));
+        odd = __any(odd);
       }
       float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(s[0][e], s[1][e]));
-      top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (__any(top > m + kSlack)) {
+      top = max_halves(top) * sm;
+      if (__builtin_expect(__any(top > m + kSlack), 0)) {
         const float mm = fmaxf(m, top), f = exp2_fast(m - mm);
         m = mm;
         l *= f;
 #pragma unroll
         for (int d = 0; d < 4; ++d) o[d] *= f;
       }
+      bf16x8 pb[4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        bf16x8 pb[2];
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x = exp2_fast(s[n][e] - m);
+          const float x = exp2_fast(fmaf(s[n][e], sm, -m));
           l += x;  // the total keeps 32 bits; the weights are rounded to bf16 for the matrix cores
-          pb[e >> 3][e & 7] = (__bf16)x;
+          pb[2 * n + (e >> 3)][e & 7] = (__bf16)x;
         }
-        // ---- sums of values 32 d + (result row) for query c
+      // ---- sums of values 32 d + (result row) for query c
+      if (__builtin_expect(!odd, 1)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(i >> 1, i & 1, d), pb[i], o[d], 0, 0, 0);
+      } else {  // each key with such a value adds it to the queries that see the key
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const int row = 32 * n + 16 * j + 4 * h2 + (lo >> 2);
-            const int ch = kNope / 8 + 4 * d + 2 * ((lane >> 4) & 1) + ((lo & 3) >> 1);
-            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(tb + row * kKvRow + (ch ^ swz_kv(row)) * 16 + (lo & 1) * 8));
-            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(tb + (row + 8) * kKvRow + (ch ^ swz_kv(row + 8)) * 16 + (lo & 1) * 8));
-            bf16x8 a = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-            if (mixed && __any(any_odd(a))) {
-              // each key with such a value adds it to the queries that see the key
-              for (int k = 0; k < 16; ++k) {
-                const bf16x8 one = part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1);
-                f32x16 z;
+            const bf16x8 a = values(i >> 1, i & 1, d);
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              const bf16x8 one = part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1);
+              f32x16 z;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z[e] = 0.f;
-                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, pb[j], z, 0, 0, 0);
-                const int key = k0 + 32 * n + 16 * j + 8 * ((k & 7) >> 2) + 4 * (k >> 3) + (k & 3);
-                if (key >= s_lo && key < s_hi) o[d] += z;
-              }
-              a = part_of<false>(a, 0);
+              for (int e = 0; e < 16; ++e) z[e] = 0.f;
+              z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, pb[i], z, 0, 0, 0);
+              const int key = k0 + 16 * i + 8 * ((k & 7) >> 2) + 4 * (k >> 3) + (k & 3);
+              if (key >= s_lo && key < s_hi) o[d] += z;
             }
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pb[j], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part_of<false>(a, 0), pb[i], o[d], 0, 0, 0);
           }
       }
     }
@@ -205,7 +225,7 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   }
 
   // ---- result: lane holds values 32 d + 8 i + 4 h2 + 0..3 of query c
-  const float tot = l + __shfl_xor(l, 32, kWave);
+  const float tot = sum_halves(l);
   if (t >= p.T) return;
   const int64_t R = (int64_t)t * p.H + head;
   if (p.splits > 1) {
