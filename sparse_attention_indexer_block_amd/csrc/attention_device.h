@@ -37,11 +37,12 @@ __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
       : "s"(lds), "v"(src)
       : "memory");
 }
-// The same from base + off, base uniform over the wave.
+// The same from base + off, base uniform over the wave. It may come from a lane
+// read, after which a memory instruction has to wait five states for it.
 __device__ __forceinline__ void copy16_to_lds_at(const void* base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
+      "s_nop 4\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(off), "s"(base)
@@ -121,6 +122,9 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(u32x2 v) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// (The sums of such a tile go through thread-private memory, which lets the
+// rare path be a loop: it costs the common one no registers.)
+
 // Keys 0 .. pos of a prefix of `left` keys (0 for pos < 0).
 __device__ __forceinline__ int visible_keys(int pos, int left) { return pos < 0 ? 0 : (pos < left ? pos + 1 : left); }
 
@@ -137,6 +141,14 @@ __device__ __forceinline__ void mfma_vgpr(f32x16& d, bf16x8 a, bf16x8 b) {
   asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void mfma_done(f32x16& d) { asm volatile("s_nop 15" : "+v"(d)); }
+
+// The same value, taken anew: what is derived from it is formed where it is
+// used, instead of once before the loop and kept in registers.
+template <typename Tp>
+__device__ __forceinline__ Tp anew(Tp x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // Keeps an accumulator in the accumulation registers on both sides of this
 // point: at the entry of a rare branch that changes it, the copies that the

@@ -141,24 +141,27 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
       const uint32_t ka = tb + a_key, ra = tb + a_rot, va = tb + a_val;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lds_read<bf16x8>((ka ^ (32 * ks)) + n * 32 * kKvRow), qf[ks],
-                                                         s[n], 0, 0, 0);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          s[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lds_read<bf16x8>((ra ^ (32 * ks)) + n * 32 * 2 * kRotary),
-                                                         qf[8 + ks], s[n], 0, 0, 0);
-      // value operand of step (n, j): keys 32 n + 16 j .. + 15, values 32 d .. + 31
-      auto values = [&](int n, int j, int d) -> bf16x8 {
-        const uint32_t at = va ^ (64 * d) ^ (256 * j);
-        const int off = (32 * n + 16 * j) * kKvRow;
-        return join_rows(lds_read_tr16(at + off), lds_read_tr16((at ^ 32) + off + 8 * kKvRow));
+      // Operand reads run kAhead steps before their products, in one sequence:
+      // key rows 32 n + c of K step ks (2 ks + n), then values 32 d .. + 31 of
+      // keys 16 i .. + 15 (4 i + d)
+      constexpr int kKeyReads = 24, kAhead = 8;
+      bf16x8 ring[kAhead];
+      auto read = [&](int i) -> bf16x8 {
+        if (i < 16) return lds_read<bf16x8>((ka ^ (32 * (i >> 1))) + (i & 1) * 32 * kKvRow);
+        if (i < 24) return lds_read<bf16x8>((ra ^ (32 * ((i >> 1) - 8))) + (i & 1) * 32 * 2 * kRotary);
+        const int k = (i - 24) >> 2, d = (i - 24) & 3;
+        const uint32_t at = va ^ (64 * d) ^ (256 * (k & 1));
+        return join_rows(lds_read_tr16(at + 16 * k * kKvRow), lds_read_tr16((at ^ 32) + (16 * k + 8) * kKvRow));
       };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < kKeyReads; ++i) {
+        s[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i % kAhead], qf[i >> 1], s[i & 1], 0, 0, 0);
+        ring[i % kAhead] = read(i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
       const bool mixed = k0 < f_lo || k0 + kAttnTile > f_hi;  // not every query sees every key
       bool odd = false;                                       // and a value is not finite
       if (__builtin_expect(mixed, 0)) {
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
             s[n][e] = key >= s_lo && key < s_hi ? s[n][e] : -INFINITY;
           }
 #pragma unroll 1
-        for (int i = 0; i < 16; ++i) odd |= any_odd(values(i >> 3, (i >> 2) & 1, i & 3));
+        for (int i = 0; i < 16; ++i) odd |= any_odd(read(kKeyReads + i));
         odd = __any(odd);
       }
       float top = fmaxf(s[0][0], s[1][0]);
@@ -196,16 +199,17 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
       // ---- sums of values 32 d + (result row) for query c
       if (__builtin_expect(!odd, 1)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(i >> 1, i & 1, d), pb[i], o[d], 0, 0, 0);
+        for (int i = 0; i < 16; ++i) {
+          o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(kKeyReads + i) % kAhead], pb[i >> 2], o[i & 3], 0, 0, 0);
+          if (i + kAhead < 16) ring[(kKeyReads + i) % kAhead] = read(kKeyReads + i + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       } else {  // each key with such a value adds it to the queries that see the key
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const bf16x8 a = values(i >> 1, i & 1, d);
+            const bf16x8 a = read(kKeyReads + 4 * i + d);
 #pragma unroll 1
             for (int k = 0; k < 16; ++k) {
               const bf16x8 one = part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1);

@@ -7,6 +7,7 @@
 // list or over its visible keys. All heads of a query read the same keys, and
 // a key row is its own value row.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention_device.h"
@@ -41,18 +42,44 @@ struct LatentTile {
   static __device__ __forceinline__ int swz_rope(int row) { return WIDE ? (row >> 2) & 7 : ((row >> 2) & 3) << 1; }
 };
 
-// Where a workgroup's rows and keys are, and the walk over its key tiles.
-template <int NQ, bool LIST>
+// Where a workgroup's rows and keys are, and the walk over its key tiles. Rows
+// come in units of U heads of one query, so that the rows of a unit see the
+// same keys; the units of a workgroup belong to one query, or (units of queries
+// that share their keys) to consecutive ones.
+template <int NQ, int U, bool LIST>
 struct LatentWork {
   const LatentArgs& p;
   int lane;
-  int64_t r0;      // first row (query * H + head)
-  int nv, t;       // rows; their query (when head_tiles)
+  int rt, t;       // row tile; its query (when head_tiles)
   int base;
-  int j1;          // entries of the list, or visible keys of the rows that see most
-  int same;        // keys that every row sees (prefix form)
+  int j1;          // entries of the list, or visible keys of the unit that sees most
+  int same;        // keys that every unit sees (prefix form)
+  i32x4 ulim;      // visible keys of each unit (units of several queries)
+  static_assert(NQ / U <= 4, "at most four units");
   int split, cur, tile_end;
   bool valid;
+
+  struct Unit {
+    int64_t row;   // first row (query * H + head)
+    int rows, lim; // rows (0: none), visible keys (prefix form)
+  };
+  __device__ __forceinline__ Unit unit(int i) const {
+    const int hc = (p.H + U - 1) / U;
+    int tu = t, c;
+    if (p.head_tiles) {
+      c = (rt % p.head_tiles) * (NQ / U) + i;
+    } else {
+      const int64_t g = (int64_t)rt * (NQ / U) + i;
+      tu = (int)(g / hc);
+      c = (int)(g % hc);
+    }
+    Unit u{0, 0, 0};
+    if (tu >= p.T || c >= hc) return u;
+    u.row = (int64_t)tu * p.H + c * U;
+    u.rows = min(U, p.H - c * U);
+    if constexpr (!LIST) u.lim = p.head_tiles ? j1 : visible_keys(p.pos[tu], left());
+    return u;
+  }
 
   __device__ __forceinline__ LatentWork(const LatentArgs& a, int lane_) : p(a), lane(lane_) {
     // neighbouring workgroups run on different XCDs; give each XCD a run of
@@ -60,21 +87,11 @@ struct LatentWork {
     const int per = (int)(gridDim.x / 8);
     const int lid = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
     const int ht = p.head_tiles ? p.head_tiles : 1;
-    const int rt = (lid / (ht * p.splits)) * ht + lid % ht;
+    rt = (lid / (ht * p.splits)) * ht + lid % ht;
     split = (lid / ht) % p.splits;
     valid = rt < p.row_tiles;
     if (!valid) return;
-    const int64_t nrows = (int64_t)p.T * p.H;
-    t = 0;
-    if (p.head_tiles) {
-      t = rt / p.head_tiles;
-      const int h0 = (rt % p.head_tiles) * NQ;
-      r0 = (int64_t)t * p.H + h0;
-      nv = min(NQ, p.H - h0);
-    } else {
-      r0 = (int64_t)rt * NQ;
-      nv = (int)min((int64_t)NQ, nrows - r0);
-    }
+    t = p.head_tiles ? rt / p.head_tiles : 0;
     base = (p.base && p.head_tiles) ? p.base[t] : 0;
     same = 0x7fffffff;
     if constexpr (LIST) {
@@ -84,23 +101,23 @@ struct LatentWork {
     } else {
       j1 = 0;
 #pragma unroll
-      for (int i = 0; i < (NQ + 63) / 64; ++i) {
-        const int r = 64 * i + lane;
-        const int n = r < nv ? visible_keys(p.pos[(r0 + r) / p.H], left()) : -1;
-        j1 = max(j1, n);
-        same = n >= 0 ? min(same, n) : same;
+      for (int i = 0; i < NQ / U; ++i) {
+        const Unit u = unit(i);
+        ulim[i] = __builtin_amdgcn_readfirstlane(u.lim);
+        j1 = max(j1, u.lim);
+        same = u.rows ? min(same, u.lim) : same;
       }
-      j1 = __builtin_amdgcn_readfirstlane((int)wave_max_u32((uint32_t)j1));
-      same = __builtin_amdgcn_readfirstlane((int)wave_min_u32((uint32_t)same));
     }
     j1 = __builtin_amdgcn_readfirstlane(j1);
+    same = __builtin_amdgcn_readfirstlane(same);
     tile_end = min((j1 + kAttnTile - 1) / kAttnTile, (split + 1) * p.tiles_per_split);
     cur = split * p.tiles_per_split;
   }
   __device__ __forceinline__ int left() const { return base < 0 ? 0 : max(0, p.rows - base); }
-  // visible keys of row r (prefix form)
-  __device__ __forceinline__ int limit(int r) const {
-    return p.head_tiles ? j1 : r < nv ? visible_keys(p.pos[(r0 + r) / p.H], left()) : 0;
+  // keys of tile ti (bits) that a unit with limit lim sees, of those that the tile holds
+  __device__ __forceinline__ uint64_t sees(int ti, int lim, uint64_t held) const {
+    const int n = lim - ti * kAttnTile;
+    return n >= kAttnTile ? held : n <= 0 ? 0 : held & ((1ull << n) - 1);
   }
   // entry 64 * ti + lane of the list
   __device__ __forceinline__ int list_entry(int ti) const {
@@ -132,43 +149,90 @@ struct LatentWork {
   }
 };
 
-// Copies key rows 16 w .. 16 w + 15 of a tile to LDS at dst; lane i of `rows`
-// holds the cache row of the tile's key i, or -1 (zeros then).
-template <class Tile, bool FP8>
-__device__ __forceinline__ void stage_tile(const LatentArgs& p, uint32_t dst, int w, int lane, int rows) {
-  const unsigned char* C = static_cast<const unsigned char*>(p.c);
-  const unsigned char* zero = reinterpret_cast<const unsigned char*>(g_zero_row);
-  if constexpr (FP8) {
+// Masks for an operand of eight bf16 values: element e stays if bit key(e) of
+// `keep` is set.
+template <typename Key>
+__device__ __forceinline__ u32x4 keep_mask(uint64_t keep, Key key) {
+  u32x4 m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // two rows a copy
-      const int row = 16 * w + 2 * i + (lane >> 5);
-      const int s = __shfl(rows, row, kWave);
-      const int ch = (lane & 31) ^ Tile::swz(row);
-      const unsigned char* src = s >= 0 ? C + (int64_t)s * kLatent : zero;
-      copy16_to_lds(src + ch * 16, dst + (16 * w + 2 * i) * Tile::kRow);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int row = 16 * w + i;
-      const int s = __builtin_amdgcn_readlane(rows, row);
-      const unsigned char* src = s >= 0 ? C + (int64_t)s * (2 * (kLatent + kRotary)) : zero;
-      copy16_to_lds_at(src, (lane ^ Tile::swz(row)) * 16, dst + row * Tile::kRow);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {  // eight rotary rows a copy
-    const int row = 16 * w + 8 * i + (lane >> 3);
-    const int s = __shfl(rows, row, kWave);
-    const int ch = (lane & 7) ^ Tile::swz_rope(row);
-    const unsigned char* src;
-    if constexpr (FP8)
-      src = s >= 0 ? reinterpret_cast<const unsigned char*>(p.rope) + (int64_t)s * (2 * kRotary) : zero;
-    else
-      src = s >= 0 ? C + (int64_t)s * (2 * (kLatent + kRotary)) + 2 * kLatent : zero;
-    copy16_to_lds(src + ch * 16, dst + Tile::kRope + (16 * w + 8 * i) * Tile::kRopeRow);
-  }
+  for (int i = 0; i < 4; ++i)
+    m[i] = ((keep >> key(2 * i)) & 1 ? 0xffffu : 0u) | ((keep >> key(2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+  return m;
 }
+__device__ __forceinline__ bf16x8 masked(bf16x8 a, u32x4 m) {
+  return __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, a) & m);
+}
+
+// Copies a tile to LDS, one instruction (1 KB) at a time: a wave that issues them
+// back to back stalls, so they are spread over the products of the tile before.
+// Wave w copies key rows 16 w .. 16 w + 15. aim() takes the tile's cache rows (lane
+// i: key i, or -1, which reads zeros) and leaves little to do per copy.
+template <class Tile, bool FP8>
+struct TileCopy {
+  static constexpr int kPerEight = FP8 ? 5 : 9;  // copies of eight rows: the rows, then their rotary values
+  static constexpr int kCopies = 2 * kPerEight;
+  const LatentArgs& p;
+  int w, lane;
+  uint64_t mine;       // address of key row `lane`
+  int rot[2];          // the lane's rotary rows, counted from rot_base
+  uint64_t rot_base;
+
+  __device__ __forceinline__ uint64_t address(const void* from, int row, int stride, int offset) const {
+    return row >= 0 ? (uint64_t)(uintptr_t)from + (uint64_t)(uint32_t)row * (uint32_t)stride + offset
+                    : (uint64_t)(uintptr_t)g_zero_row;
+  }
+  // copies from q instead, with the layout of bf16 key rows: row i is row i % 32 of unit u0 or u1
+  template <typename Unit>
+  __device__ __forceinline__ void aim_q(const Unit& u0, const Unit& u1) {
+    static_assert(!FP8, "queries are bf16 rows");
+    constexpr int kStride = 2 * (kLatent + kRotary);
+    mine = (lane & 31) < (lane < 32 ? u0.rows : u1.rows)
+               ? (uint64_t)(uintptr_t)p.q + (uint64_t)((lane < 32 ? u0.row : u1.row) + (lane & 31)) * kStride
+               : (uint64_t)(uintptr_t)g_zero_row;
+    rot_base = (uint64_t)(uintptr_t)p.q + (uint64_t)(w < 2 ? u0.row : u1.row) * kStride;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * (w & 1) + 8 * i + (lane >> 3);
+      rot[i] = r < (w < 2 ? u0.rows : u1.rows) ? r : -1;
+    }
+  }
+  __device__ __forceinline__ void aim(int rows) {
+    rot_base = (uint64_t)(uintptr_t)(FP8 ? (const void*)p.rope : p.c);
+    mine = address(p.c, rows, FP8 ? kLatent : 2 * (kLatent + kRotary), 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rot[i] = __shfl(rows, 16 * w + 8 * i + (lane >> 3), kWave);
+  }
+  __device__ __forceinline__ uint64_t row_address(int i) const {
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)mine, i);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(mine >> 32), i);
+    return (uint64_t)hi << 32 | lo;
+  }
+  // copy j of the wave's rows 8 half .. 8 half + 7
+  __device__ __forceinline__ void copy(uint32_t dst, int half, int j) const {
+    const int r0 = 16 * w + 8 * half;
+    if (j < kPerEight - 1) {
+      if constexpr (FP8) {  // two rows a copy
+        const uint64_t a0 = row_address(r0 + 2 * j), a1 = row_address(r0 + 2 * j + 1);
+        const int row = r0 + 2 * j + (lane >> 5);
+        const uint64_t src = (lane < 32 ? a0 : a1) + (((lane & 31) ^ Tile::swz(row)) * 16);
+        copy16_to_lds(reinterpret_cast<const void*>(src), dst + (r0 + 2 * j) * Tile::kRow);
+      } else {
+        copy16_to_lds_at(reinterpret_cast<const void*>(row_address(r0 + j)), (lane ^ Tile::swz(r0 + j)) * 16,
+                         dst + (r0 + j) * Tile::kRow);
+      }
+    } else {
+      const int row = r0 + (lane >> 3), s = half ? rot[1] : rot[0];
+      const void* from = reinterpret_cast<const void*>(rot_base);
+      const uint64_t src = FP8 ? address(from, s, 2 * kRotary, 0) : address(from, s, 2 * (kLatent + kRotary), 2 * kLatent);
+      copy16_to_lds(reinterpret_cast<const void*>(src + (((lane & 7) ^ Tile::swz_rope(row)) * 16)),
+                    dst + Tile::kRope + r0 * Tile::kRopeRow);
+    }
+  }
+  __device__ __forceinline__ void all(uint32_t dst) const {
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) copy(dst, j / kPerEight, j % kPerEight);
+  }
+};
 
 // NQ = 16 or 32 rows and a share of the keys per workgroup of four waves. Per
 // tile of 64 keys: wave w scores keys 16 w .. 16 w + 15 against all NQ rows (S^T
@@ -190,16 +254,16 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lo = lane & 15, g = lane >> 4;
 
-  LatentWork<NQ, LIST> wk(p, lane);
+  LatentWork<NQ, 16, LIST> wk(p, lane);
   if (!wk.valid) return;
-  const int64_t r0 = wk.r0, nrows = (int64_t)p.T * p.H;
-  const int nv = wk.nv, tile_end = wk.tile_end;
-  int lim[QT];  // visible keys of each of the lane's rows
+  const int64_t nrows = (int64_t)p.T * p.H;
+  const int tile_end = wk.tile_end;
+  typename LatentWork<NQ, 16, LIST>::Unit un[QT];
 #pragma unroll
-  for (int i = 0; i < QT; ++i) lim[i] = LIST ? 0 : wk.limit(i * 16 + lo);
+  for (int i = 0; i < QT; ++i) un[i] = wk.unit(i);
 
   const uint32_t tile_lds = lds_addr(&tile[0][0]);
-  auto stage = [&](int b, int rows) { stage_tile<Tile, FP8>(p, tile_lds + b * Tile::kBytes, w, lane, rows); };
+  TileCopy<Tile, FP8> copies{p, w, lane};
   auto key_scale = [&](int rows) -> float {
     if constexpr (FP8) return rows >= 0 ? p.scale[rows] : 0.f;
     return 0.f;
@@ -209,7 +273,9 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   int cur = wk.find_tile(wk.cur, wk.list_entry(wk.cur), rows_cur);
   int nxt = wk.find_tile(cur + 1, wk.list_entry(cur + 1), rows_nxt);
   float sc_cur = key_scale(rows_cur);
-  if (cur < tile_end) stage(0, rows_cur);
+  copies.aim(rows_cur);
+  if (cur < tile_end) copies.all(tile_lds);
+  copies.aim(rows_nxt);
 
   // Q as the B operand: lane (row lo, group g) of K step ks holds values
   // 32 ks + 8 g .. + 7; with codes, whose 16-byte chunk covers two K steps,
@@ -218,9 +284,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   bf16x8 qf[QT][18];
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
-    const int r = i * 16 + lo;
     const uint32_t sign = p.sm_log2 < 0.f ? 0x80008000u : 0u;
-    const uint16_t* qr = p.q + (r0 + min(r, nv - 1)) * (kLatent + kRotary);
+    const uint16_t* qr = p.q + (un[i].row + min(lo, max(un[i].rows - 1, 0))) * (kLatent + kRotary);
 #pragma unroll
     for (int ks = 0; ks < 18; ++ks) {
       const int at = (FP8 && ks < 16) ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
@@ -256,14 +321,23 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   const uint32_t a_pwr = pt_lds + lo * 128 + (((2 * w + (g >> 1)) ^ (lo & 7)) * 16) + (g & 1) * 8;
 
   int it = 0;
-  while (cur < tile_end) {
+  // one tile; PART: not every unit sees every key that the tile holds
+  auto step = [&](auto part) {
+    constexpr bool PART = decltype(part)::value;
     const uint32_t tb = tile_lds + (it & 1) * Tile::kBytes;
-    const bool mixed = !LIST && (cur + 1) * kAttnTile > wk.same;  // not every row sees every key
     // the list entries after the next tile and the next tile's scales are asked
     // for ahead of its copy and used after the copy has landed
     const int v_nn = wk.list_entry(nxt + 1);
     const float sc_nxt = key_scale(rows_nxt);
-    if (nxt < tile_end) stage((it + 1) & 1, rows_nxt);
+    copies.lane = anew(lane);
+    const uint32_t next_lds = tile_lds + ((it + 1) & 1) * Tile::kBytes;  // (no next tile: zeros, unused)
+    // the next tile's copies, spread over the 16 products of the scores and the 16 of the sums
+    auto spread = [&](int i) {
+      using Copy = TileCopy<Tile, FP8>;
+#pragma unroll
+      for (int j = i * Copy::kCopies / 32; j < (i + 1) * Copy::kCopies / 32; ++j)
+        copies.copy(next_lds, j / Copy::kPerEight, j % Copy::kPerEight);
+    };
 
     // ---- scores of keys 16 w + 4 g + 0..3 (result rows) for rows 16 i + lo (columns)
     f32x4 s[QT];
@@ -279,6 +353,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         for (int i = 0; i < QT; ++i) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, qf[i][2 * c], s[i], 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < QT; ++i) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, qf[i][2 * c + 1], s[i], 0, 0, 0);
+        spread(2 * c);
+        spread(2 * c + 1);
       }
     } else {
 #pragma unroll
@@ -286,6 +362,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         const bf16x8 a = lds_read<bf16x8>((ka ^ (64 * (ks & 7))) + 512 * (ks >> 3));
 #pragma unroll
         for (int i = 0; i < QT; ++i) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, qf[i][ks], s[i], 0, 0, 0);
+        spread(ks);
       }
     }
     f32x4 ksc;
@@ -303,14 +380,16 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
     }
 
     // ---- weights against the present reference
-    const uint64_t live = wave_ballot(rows_cur >= 0);
-    const uint32_t mine = (uint32_t)(live >> (16 * w + 4 * g)) & 15u;
+    const uint64_t held = wave_ballot(rows_cur >= 0);
+    uint64_t seen[QT];
+#pragma unroll
+    for (int i = 0; i < QT; ++i) seen[i] = PART ? wk.sees(cur, un[i].lim, held) : held;
     bool high = false;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool ok = LIST ? (mine >> e) & 1u : cur * kAttnTile + 16 * w + 4 * g + e < lim[i];
+        const bool ok = (seen[i] >> (16 * w + 4 * g + e)) & 1u;
         s[i][e] = ok ? s[i][e] : -INFINITY;
       }
       const float top = max_over_groups(fmaxf(fmaxf(s[i].x, s[i].y), fmaxf(s[i].z, s[i].w))) * sm;
@@ -328,7 +407,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         // rounded to bf16 for the matrix cores; the row's total keeps 32 bits
         if constexpr (FP8) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) e[x] = mixed && e[x] == 0.f ? 0.f : e[x] * ksc[x];
+          for (int x = 0; x < 4; ++x) e[x] = PART && e[x] == 0.f ? 0.f : e[x] * ksc[x];
         }
         *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(a_pwr + i * 2048) = __builtin_convertvector(e, bf16x4);
       }
@@ -365,41 +444,22 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         return join_rows(lds_read_tr16((va ^ (32 * d)) + 32 * j * Tile::kRow),
                          lds_read_tr16((va ^ (32 * d) ^ 256) + (32 * j + 4) * Tile::kRow));
     };
-    bool odd = false;
-    if (__builtin_expect(mixed, 0)) {
-#pragma unroll 1
-      for (int i = 0; i < 16; ++i) odd |= any_odd(values(i >> 3, i & 7));
-      odd = __any(odd);
-    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       bf16x8 pb[QT];
+      u32x4 keep[QT];  // a key that a unit does not see is no value for it, whatever it holds
 #pragma unroll
-      for (int i = 0; i < QT; ++i) pb[i] = lds_read<bf16x8>((a_prd ^ (64 * j)) + i * 2048);
-      if (__builtin_expect(!odd, 1)) {
+      for (int i = 0; i < QT; ++i) {
+        pb[i] = lds_read<bf16x8>((a_prd ^ (64 * j)) + i * 2048);
+        if constexpr (PART) keep[i] = keep_mask(seen[i], [&](int e) { return 32 * j + 8 * g + e; });
+      }
 #pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          const bf16x8 a = values(j, d);
+      for (int d = 0; d < 8; ++d) {
+        const bf16x8 a = values(j, d);
 #pragma unroll
-          for (int i = 0; i < QT; ++i) o[d][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, pb[i], o[d][i], 0, 0, 0);
-        }
-      } else {  // each key with a value that is not finite adds it to the rows that see the key
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          const bf16x8 a = values(j, d);
-#pragma unroll 1
-          for (int k = 0; k < 32; ++k) {
-            const bf16x8 one = part_of<true>(a, g == (k >> 3) ? (k & 7) : -1);
-#pragma unroll
-            for (int i = 0; i < QT; ++i) {
-              const f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, pb[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-              if (cur * kAttnTile + 32 * j + k < lim[i]) o[d][i] += z;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < QT; ++i)
-            o[d][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part_of<false>(a, 0), pb[i], o[d][i], 0, 0, 0);
-        }
+        for (int i = 0; i < QT; ++i)
+          o[d][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(PART ? masked(a, keep[i]) : a, pb[i], o[d][i], 0, 0, 0);
+        spread(16 + 8 * j + d);
       }
     }
     wait_copies();
@@ -408,7 +468,12 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
     rows_cur = rows_nxt;
     sc_cur = sc_nxt;
     nxt = wk.find_tile(nxt + 1, v_nn, rows_nxt);
+    copies.aim(rows_nxt);
     ++it;
+  };
+  while (cur < tile_end && (LIST || (cur + 1) * kAttnTile <= wk.same)) step(std::false_type{});
+  if constexpr (!LIST) {
+    while (cur < tile_end) step(std::true_type{});
   }
 
   // ---- totals over the waves, then the result
@@ -422,8 +487,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   for (int i = 0; i < QT; ++i) {
     const int r = i * 16 + lo;
     const float tot = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
-    if (r >= nv) continue;
-    const int64_t R = r0 + r;
+    if (lo >= un[i].rows) continue;
+    const int64_t R = un[i].row + lo;
     if (p.splits > 1) {
       float* po = p.part + ((int64_t)wk.split * nrows + R) * kLatent + 128 * w + 4 * g;
 #pragma unroll
@@ -449,11 +514,15 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // weights never leave the lanes that formed them (result rows of S^T = C Q^T are
 // keys; the contraction of O^T = C^T P^T takes the keys in that order). With G =
 // 4 a tile serves 128 rows. With G = 2 the two waves of a row group take
-// alternate halves of each tile and are joined at the end.
+// alternate halves of each tile and are joined at the end. Where the units of a
+// workgroup see different numbers of keys (queries side by side in the prefix
+// form), the few tiles that not all of them see in full are taken once for each
+// number, with the keys beyond it left out, by the waves that it belongs to.
 template <int G, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   using Tile = LatentTile<FP8, true>;
   constexpr int NQ = 32 * G, NS = G / 2;  // rows; 32-key steps of a wave per tile
+  constexpr int kAhead = 6;               // LDS reads in flight
   __shared__ __attribute__((aligned(1024))) unsigned char tile[2][Tile::kBytes];
   __shared__ __attribute__((aligned(16))) float ksc[2][kAttnTile];
 
@@ -462,39 +531,106 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   const int c = lane & 31, h2 = lane >> 5, lo = lane & 15;
   const int grp = w % G, half = w / G;  // row group, key half of a tile (G = 2)
 
-  LatentWork<NQ, LIST> wk(p, lane);
+  LatentWork<NQ, 32, LIST> wk(p, lane);
   if (!wk.valid) return;
-  const int64_t r0 = wk.r0, nrows = (int64_t)p.T * p.H;
-  const int nv = wk.nv, tile_end = wk.tile_end;
-  const int r = 32 * grp + c;  // the lane's row
-  const int lim = LIST ? 0 : wk.limit(r);
+  const int64_t nrows = (int64_t)p.T * p.H;
+  const int tile_end = wk.tile_end;
+  const auto un = wk.unit(grp);  // the wave's rows; lane's row un.row + c
 
   const uint32_t tile_lds = lds_addr(&tile[0][0]);
-  auto stage = [&](int b, int rows) { stage_tile<Tile, FP8>(p, tile_lds + b * Tile::kBytes, w, lane, rows); };
+  TileCopy<Tile, FP8> copies{p, w, lane};
   auto key_scale = [&](int rows) -> float {
     if constexpr (FP8) return w == 0 && rows >= 0 ? p.scale[rows] : 0.f;
     return 0.f;
   };
 
+  // the pass after (tile, number): the next tile that holds a key, or the next
+  // number of a tile that is taken by number (who: the unit it is of, -1: all)
+  auto next_pass = [&](int ti, int who, int v, int& who_next, int& rows) -> int {
+    if constexpr (!LIST) {
+      if (!p.head_tiles) {
+        ++who;
+        for (; ti < tile_end; ++ti, who = 0) {
+          if ((ti + 1) * kAttnTile <= wk.same) {
+            who_next = -1;
+            rows = wk.row_of(ti, 0);
+            return ti;
+          }
+#pragma unroll
+          for (int u = 0; u < G; ++u) {
+            bool first = u >= who && wk.ulim[u] > ti * kAttnTile;
+#pragma unroll
+            for (int x = 0; x < u; ++x) first = first && wk.ulim[x] != wk.ulim[u];
+            if (first) {
+              who_next = u;
+              const int j = ti * kAttnTile + lane;
+              rows = j < wk.ulim[u] ? j : -1;
+              return ti;
+            }
+          }
+        }
+        who_next = -1;
+        rows = -1;
+        return ti;
+      }
+    }
+    who_next = -1;
+    return wk.find_tile(ti, v, rows);
+  };
+  auto ulim_of = [&](int who) {
+    int x = wk.ulim[0];
+#pragma unroll
+    for (int u = 1; u < G; ++u) x = who == u ? wk.ulim[u] : x;
+    return x;
+  };
+  // (a tile taken by number may have another pass)
+  auto after = [&](int ti, int who) { return who < 0 ? ti + 1 : ti; };
   int rows_cur, rows_nxt;
-  int cur = wk.find_tile(wk.cur, wk.list_entry(wk.cur), rows_cur);
-  int nxt = wk.find_tile(cur + 1, wk.list_entry(cur + 1), rows_nxt);
+  int who_cur, who_nxt;
+  int cur = next_pass(wk.cur, -1, wk.list_entry(wk.cur), who_cur, rows_cur);
+  int nxt = next_pass(after(cur, who_cur), who_cur, wk.list_entry(cur + 1), who_nxt, rows_nxt);
   if (FP8 && w == 0) ksc[0][lane] = key_scale(rows_cur);
-  if (cur < tile_end) stage(0, rows_cur);
 
   // Q as the B operand: K step ks, lane (row c, half h2): values 16 ks + 8 h2 .. + 7; with
-  // codes, whose 16-byte chunk covers two K steps, 32 (ks / 2) + 16 h2 + 8 (ks % 2) .. + 7
+  // codes, whose 16-byte chunk covers two K steps, 32 (ks / 2) + 16 h2 + 8 (ks % 2) .. + 7.
+  // The rows come through LDS in the layout of bf16 key rows, 64 at a time: loads of
+  // 16 bytes a row would touch 32 lines each.
   const float sm = scale_magnitude(p.sm_log2);
   bf16x8 qf[36];
   {
+    using QTile = LatentTile<false, true>;
+    constexpr int kFit = FP8 ? 1 : 2;  // tiles of 64 rows that fit at once
+    static_assert(kFit * QTile::kBytes <= 2 * Tile::kBytes, "query rows fit the key tiles");
+    TileCopy<QTile, false> qc{p, w, lane};
     const uint32_t sign = p.sm_log2 < 0.f ? 0x80008000u : 0u;
-    const uint16_t* qr = p.q + (r0 + min(r, nv - 1)) * (kLatent + kRotary);
+    const int qrow = 32 * (grp & 1) + c;
 #pragma unroll
-    for (int ks = 0; ks < 36; ++ks) {
-      const int at = (FP8 && ks < 32) ? 32 * (ks >> 1) + 16 * h2 + 8 * (ks & 1) : 16 * ks + 8 * h2;
-      qf[ks] = flip_sign(*reinterpret_cast<const bf16x8*>(qr + at), sign);
+    for (int q0 = 0; q0 < NQ / 64; q0 += kFit) {
+#pragma unroll
+      for (int i = q0; i < q0 + kFit && i < NQ / 64; ++i) {
+        qc.aim_q(wk.unit(2 * i), wk.unit(2 * i + 1));
+        qc.all(tile_lds + (i - q0) * QTile::kBytes);
+      }
+      wait_copies();
+      __syncthreads();
+      if (grp / 2 >= q0 && grp / 2 < q0 + kFit) {
+        const uint32_t qb = tile_lds + (grp / 2 - q0) * QTile::kBytes + qrow * QTile::kRow;
+        const uint32_t qr = tile_lds + (grp / 2 - q0) * QTile::kBytes + QTile::kRope + qrow * QTile::kRopeRow;
+#pragma unroll
+        for (int ks = 0; ks < 36; ++ks) {
+          const int ch = FP8 ? 4 * (ks >> 1) + (ks & 1) : 2 * ks;
+          const uint32_t at = ks < 32 ? ((qb + (((FP8 ? 2 * h2 : h2) ^ QTile::swz(qrow)) * 16)) ^ (16 * (ch & 31))) + 512 * (ch >> 5)
+                                      : (qr + ((h2 ^ QTile::swz_rope(qrow)) * 16)) ^ (32 * (ks - 32));
+          qf[ks] = flip_sign(lds_read<bf16x8>(at), sign);
+        }
+      }
+      lds_barrier();
     }
   }
+  copies.aim(rows_cur);
+  if (cur < tile_end) copies.all(tile_lds);
+  copies.aim(rows_nxt);
+
   f32x16 o[16];
 #pragma unroll
   for (int d = 0; d < 16; ++d)
@@ -517,75 +653,89 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   int it = 0;
   while (cur < tile_end) {
     const uint32_t tb = tile_lds + (it & 1) * Tile::kBytes;
-    const bool mixed = !LIST && (cur + 1) * kAttnTile > wk.same;
     const int v_nn = wk.list_entry(nxt + 1);
     const float sc_nxt = key_scale(rows_nxt);
-    if (nxt < tile_end) stage((it + 1) & 1, rows_nxt);
-    const uint64_t live = wave_ballot(rows_cur >= 0);
+    copies.lane = anew(lane);
+    const uint32_t next_lds = tile_lds + ((it + 1) & 1) * Tile::kBytes;  // (no next tile: zeros, unused)
+    const uint64_t held = wave_ballot(rows_cur >= 0);
+    const bool mine_to_do = LIST || who_cur < 0 || un.lim == ulim_of(who_cur);
+    if (!LIST && !mine_to_do) copies.all(next_lds);
 
 #pragma unroll 1
-    for (int n0 = 0; n0 < NS; ++n0) {
+    for (int n0 = 0; n0 < (mine_to_do ? NS : 0); ++n0) {
       const int n = G == 2 ? half : n0;  // keys 32 n .. + 31 of the tile
       const uint32_t nb = tb + n * 32 * Tile::kRow;
       const uint32_t ka = nb + a_key, ra = tb + a_rot + n * 32 * Tile::kRopeRow, va = nb + a_val;
+      // Operand reads run kAhead steps before their products, in one sequence
+      // over the scores and the sums: first the key rows (two K steps a read with
+      // codes), then the rotary rows, then the transposed values.
+      constexpr int kKeyReads = (FP8 ? 16 : 32) + 4, kReads = kKeyReads + 32;
+      u32x4 ring[kAhead];
+      auto read = [&](int i) -> u32x4 {
+        if (i < kKeyReads - 4)
+          return FP8 ? lds_read<u32x4>(ka ^ (32 * i)) : lds_read<u32x4>((ka ^ (32 * (i & 15))) + 512 * (i >> 4));
+        if (i < kKeyReads) return lds_read<u32x4>(ra ^ (32 * (i - (kKeyReads - 4))));
+        const int j = (i - kKeyReads) >> 4, d = (i - kKeyReads) & 15;
+        if constexpr (FP8) {
+          const u32x2 v = lds_read_tr8((va ^ (32 * d) ^ (256 * j)) + 16 * j * Tile::kRow);
+          return u32x4{v.x, v.y, 0u, 0u};
+        }
+        const uint32_t at = va ^ (64 * (d & 7)) ^ (256 * j);
+        const int off = 512 * (d >> 3) + 16 * j * Tile::kRow;
+        return __builtin_bit_cast(u32x4, join_rows(lds_read_tr16(at + off), lds_read_tr16((at ^ 32) + off + 8 * Tile::kRow)));
+      };
+      // this step's share of the next tile's copies, evenly over the kReads products
+      constexpr int kMine = TileCopy<Tile, FP8>::kCopies / NS;
+      auto spread = [&](int i) {
+        if ((i + 1) * kMine / kReads != i * kMine / kReads) {
+          const int j = i * kMine / kReads;
+          copies.copy(next_lds, G == 2 ? j / TileCopy<Tile, FP8>::kPerEight : n0, j % TileCopy<Tile, FP8>::kPerEight);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 s;
       f32x4 sc4[4];
-      if constexpr (FP8) {
 #pragma unroll
-        for (int cc = 0; cc < 16; ++cc) {
-          const u32x4 v = lds_read<u32x4>(ka ^ (32 * cc));
+      for (int i = 0; i < kKeyReads; ++i) {
+        const u32x4 v = ring[i % kAhead];
+        if (FP8 && i < 16) {
           const bf16x8 a0 = codes_to_bf16(u32x2{v.x, v.y}), a1 = codes_to_bf16(u32x2{v.z, v.w});
-          if (cc == 0)
+          if (i == 0)
             mfma_vgpr_first(s, a0, qf[0]);
           else
-            mfma_vgpr(s, a0, qf[2 * cc]);
-          mfma_vgpr(s, a1, qf[2 * cc + 1]);
+            mfma_vgpr(s, a0, qf[2 * i]);
+          mfma_vgpr(s, a1, qf[2 * i + 1]);
+        } else if (i == 0) {
+          mfma_vgpr_first(s, __builtin_bit_cast(bf16x8, v), qf[0]);
+        } else {
+          mfma_vgpr(s, __builtin_bit_cast(bf16x8, v), qf[36 - kKeyReads + i]);
         }
-        // a key's scale multiplies its latent part only
-        mfma_done(s);
+        ring[i % kAhead] = read(i + kAhead);
+        spread(i);
+        if (FP8 && i == 15) {  // a key's scale multiplies its latent part only
+          mfma_done(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc4[i] = *reinterpret_cast<const f32x4*>(&ksc[it & 1][32 * n + 8 * i + 4 * h2]);
+          for (int k = 0; k < 4; ++k) {
+            sc4[k] = *reinterpret_cast<const f32x4*>(&ksc[it & 1][32 * n + 8 * k + 4 * h2]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[4 * i + e] *= sc4[i][e];
+            for (int e = 0; e < 4; ++e) s[4 * k + e] *= sc4[k][e];
+          }
         }
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < 32; ++ks) {
-          const bf16x8 a = lds_read<bf16x8>((ka ^ (32 * (ks & 15))) + 512 * (ks >> 4));
-          if (ks == 0)
-            mfma_vgpr_first(s, a, qf[0]);
-          else
-            mfma_vgpr(s, a, qf[ks]);
-        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) mfma_vgpr(s, lds_read<bf16x8>(ra ^ (32 * ks)), qf[32 + ks]);
       mfma_done(s);
 
       // ---- weights of keys 32 n + 8 (e / 4) + 4 h2 + e % 4
-      auto values = [&](int j, int d) -> bf16x8 {  // values 32 d .. + 31, keys 32 n + 16 j .. + 15
-        if constexpr (FP8)
-          return codes_to_bf16(lds_read_tr8((va ^ (32 * d) ^ (256 * j)) + 16 * j * Tile::kRow));
-        else
-          return join_rows(
-              lds_read_tr16((va ^ (64 * (d & 7)) ^ (256 * j)) + 512 * (d >> 3) + 16 * j * Tile::kRow),
-              lds_read_tr16((va ^ (64 * (d & 7)) ^ (256 * j) ^ 32) + 512 * (d >> 3) + (16 * j + 8) * Tile::kRow));
+      auto operand = [&](u32x4 v) -> bf16x8 {
+        if constexpr (FP8) return codes_to_bf16(u32x2{v.x, v.y});
+        return __builtin_bit_cast(bf16x8, v);
       };
-      const uint32_t mine = (uint32_t)(live >> (32 * n));
-      bool odd = false;
-      if (mixed || mine != 0xffffffffu) {
+      const uint32_t mine = (uint32_t)(held >> (32 * n));
+      if (mine != 0xffffffffu) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int key = 8 * (e >> 2) + 4 * h2 + (e & 3);
-          const bool ok = LIST ? (mine >> key) & 1u : cur * kAttnTile + 32 * n + key < lim;
-          s[e] = ok ? s[e] : -INFINITY;
-        }
-        if (__builtin_expect(mixed, 0)) {
-#pragma unroll 1
-          for (int i = 0; i < 32; ++i) odd |= any_odd(values(i >> 4, i & 15));
-          odd = __any(odd);
-        }
+        for (int e = 0; e < 16; ++e) s[e] = (mine >> (8 * (e >> 2) + 4 * h2 + (e & 3))) & 1u ? s[e] : -INFINITY;
       }
       float top = s[0];
 #pragma unroll
@@ -607,36 +757,17 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       for (int e = 0; e < 16; ++e) {
         float x = exp2_fast(fmaf(s[e], sm, -m));
         l += x;  // the total keeps 32 bits; the weights are rounded to bf16 for the matrix cores
-        if constexpr (FP8) x = mixed && x == 0.f ? 0.f : x * sc4[e >> 2][e & 3];
+        if constexpr (FP8) x *= sc4[e >> 2][e & 3];
         pb[e >> 3][e & 7] = (__bf16)x;
       }
       // ---- sums of values 32 d + (result row) for row c
-      if (__builtin_expect(!odd, 1)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int d = 0; d < 16; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(j, d), pb[j], o[d], 0, 0, 0);
-      } else {  // each key with a value that is not finite adds it to the rows that see the key
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int d = 0; d < 16; ++d) {
-            in_agprs(o[d]);
-            const bf16x8 a = values(j, d);
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const bf16x8 one = part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1);
-              f32x16 z;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) z[e] = 0.f;
-              z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, pb[j], z, 0, 0, 0);
-              const int key = cur * kAttnTile + 32 * n + 16 * j + 8 * ((k & 7) >> 2) + 4 * (k >> 3) + (k & 3);
-              if (key < lim) o[d] += z;
-            }
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part_of<false>(a, 0), pb[j], o[d], 0, 0, 0);
-            in_agprs(o[d]);
-          }
+      for (int i = 0; i < 32; ++i) {
+        const bf16x8 v = operand(ring[(kKeyReads + i) % kAhead]);
+        o[i & 15] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pb[i >> 4], o[i & 15], 0, 0, 0);
+        if (i + kAhead < 32) ring[(kKeyReads + i) % kAhead] = read(kKeyReads + i + kAhead);
+        spread(kKeyReads + i);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     wait_copies();
@@ -644,7 +775,9 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
     lds_barrier();
     cur = nxt;
     rows_cur = rows_nxt;
-    nxt = wk.find_tile(nxt + 1, v_nn, rows_nxt);
+    who_cur = who_nxt;
+    nxt = next_pass(after(nxt, who_cur), who_cur, v_nn, who_nxt, rows_nxt);
+    copies.aim(rows_nxt);
     ++it;
   }
 
@@ -686,31 +819,57 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
     m = mm;
     tot = tot * f0 + t1 * f1;
   }
-  if (r >= nv) return;
-  const int64_t R = r0 + r;
+  // through LDS (the wave's own part of the tiles), so that rows leave in whole
+  // lines: 16-byte chunks in an order that depends on the row, kSeg bytes of each row at a time
+  constexpr int kSeg = FP8 ? 512 : 1024, kChunks = kSeg / 16;
+  static_assert(4 * 32 * kSeg <= 2 * Tile::kBytes, "room for every wave's rows");
+  const uint32_t mine = tile_lds + w * 32 * kSeg;
+  const int rows_here = un.rows;
+  const int64_t R = un.row;
+  auto put = [&](unsigned char* dst, int64_t stride) {  // what is in LDS to rows `stride` apart
+    constexpr int kRows = 64 / kChunks;                 // rows a store
+#pragma unroll 4
+    for (int i = 0; i < rows_here; i += kRows) {
+      const int rr = i + lane / kChunks;
+      const u32x4 v = lds_read<u32x4>(mine + rr * kSeg + (((lane % kChunks) ^ (rr & 31)) * 16));
+      if (rr < rows_here) *reinterpret_cast<u32x4*>(dst + rr * stride + (lane % kChunks) * 16) = v;
+    }
+  };
   if (p.splits > 1) {
-    float* po = p.part + ((int64_t)wk.split * nrows + R) * kLatent + 4 * h2;
+    unsigned char* dst = reinterpret_cast<unsigned char*>(p.part + ((int64_t)wk.split * nrows + R) * kLatent);
+    constexpr int kD = kSeg / 128;  // accumulator tiles a pass (32 values, 128 bytes a row)
 #pragma unroll
-    for (int d = 0; d < 16; ++d)
+    for (int d0 = 0; d0 < 16; d0 += kD) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * i) =
-            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-    if (h2 == 0) {
-      p.part_ml[((int64_t)wk.split * nrows + R) * 2] = m;
-      p.part_ml[((int64_t)wk.split * nrows + R) * 2 + 1] = tot;
+      for (int d = 0; d < kD; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(mine + c * kSeg + (((8 * d + 2 * i + h2) ^ c) * 16)) =
+              f32x4{o[d0 + d][4 * i], o[d0 + d][4 * i + 1], o[d0 + d][4 * i + 2], o[d0 + d][4 * i + 3]};
+      put(dst + d0 * 128, kLatent * 4);
+    }
+    if (c < rows_here && h2 == 0) {
+      p.part_ml[((int64_t)wk.split * nrows + R + c) * 2] = m;
+      p.part_ml[((int64_t)wk.split * nrows + R + c) * 2 + 1] = tot;
     }
   } else {
     const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
-    uint16_t* po = p.out + R * kLatent + 4 * h2;
+    unsigned char* dst = reinterpret_cast<unsigned char*>(p.out + R * kLatent);
+    constexpr int kD = kSeg / 64;
 #pragma unroll
-    for (int d = 0; d < 16; ++d)
+    for (int d0 = 0; d0 < 16; d0 += kD) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 v = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
-        *reinterpret_cast<bf16x4*>(po + 32 * d + 8 * i) = __builtin_convertvector(v, bf16x4);
-      }
-    if (p.lse && h2 == 0) p.lse[R] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
+      for (int d = 0; d < kD; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x16& x = o[d0 + d];
+          const f32x4 v = {x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv};
+          *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(mine + c * kSeg + (((4 * d + i) ^ c) * 16) + h2 * 8) =
+              __builtin_convertvector(v, bf16x4);
+        }
+      put(dst + d0 * 64, kLatent * 2);
+    }
+    if (p.lse && c < rows_here && h2 == 0) p.lse[R + c] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
   }
 }
 
@@ -764,11 +923,11 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 AttnPlan latent_plan(int T, int H, int keys, bool lists, bool fp8, bool shared_keys) {
   AttnPlan pl{};
-  // rows of different queries share a tile where they read the same keys
-  const int64_t rows = shared_keys ? (int64_t)T * H : H;
-  pl.nq = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  // units of queries that read the same keys share a tile
+  const int64_t rows16 = (int64_t)cdiv(H, 16) * 16 * (shared_keys ? T : 1), rows32 = (int64_t)cdiv(H, 32) * 32 * (shared_keys ? T : 1);
+  pl.nq = rows16 <= 16 ? 16 : rows16 <= 32 ? 32 : rows32 <= 64 ? 64 : 128;
   pl.head_tiles = shared_keys ? 0 : cdiv(H, pl.nq);
-  pl.row_tiles = shared_keys ? cdiv(rows, pl.nq) : T * pl.head_tiles;
+  pl.row_tiles = shared_keys ? cdiv(pl.nq <= 32 ? rows16 : rows32, pl.nq) : T * pl.head_tiles;
   const int tiles = std::max(1, cdiv(keys, kAttnTile));
   const int want = std::max(1, 256 / std::max(1, pl.row_tiles));
   pl.tiles_per_split = std::max(1, cdiv(tiles, std::min(want, tiles)));
