@@ -332,41 +332,70 @@ def misa_hisa_topk(q, w, K, pos, B, A, m, k, k_scale=None, heads=None, ws=None, 
 # ---------------------------------------------------------------- caches and latent attention
 
 LATENT, ROTARY, NOPE, VALUE = 512, 64, 128, 128
+_BF16, _CODES = (torch.bfloat16, torch.int16), (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32 = (torch.float32,), (torch.int32,)
 
 
-def _tensor(t: Optional[torch.Tensor], name: str, dtypes, shape, device=None):
-    """Checks one argument: a contiguous GPU tensor of one of `dtypes` and of
-    `shape` (None: any size), on `device` when one is given."""
+def _refuse(t, name: str, dtypes, shape, dev: int):
+    """Says what is wrong with an argument that _arg found wrong."""
     if t is None:
         raise ValueError(f"{name} is missing")
-    _dev(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != len(shape) or any(want is not None and want != n for want, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {['any' if n is None else n for n in shape]}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, not on GPU {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-_BF16, _CODES = (torch.bfloat16, torch.int16), (torch.uint8, torch.float8_e4m3fn)
+def _arg(t, name: str, dtypes, shape, dev: int) -> int:
+    """The address of one argument: a contiguous tensor of `shape` and of one of
+    `dtypes` on GPU `dev`. (These calls take a few microseconds in all on the
+    host, so the checks are one expression and the messages are made apart.)"""
+    if t is None or t.dtype not in dtypes or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtypes, shape, dev)
+    return t.data_ptr()
+
+
+def _first(t, name: str, dtypes, dims: int):
+    """Shape and GPU of the argument that the others are measured by."""
+    if t is None or not t.is_cuda or t.dtype not in dtypes:
+        _refuse(t, name, dtypes, (), 0)
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {len(shape)}")
+    return shape, t.get_device()
+
+
+def _on(dev: int, call, *args):
+    """call(*args, current stream of GPU dev) with dev as the current GPU."""
+    if torch.cuda.current_device() == dev:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != 0:
+        _check(status)
 
 
 def make_cache(C: torch.Tensor, c_scale: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None) -> Cache:
     """Fill the C cache struct from tensors (no copies): C [rows, d + dr] bfloat16,
     or E4M3FN codes [rows, d] with c_scale [rows] float32 and, for rows with
     rotary columns, rope [rows, 64] bfloat16."""
-    _tensor(C, "C", _BF16 + _CODES, (None, None))
-    rows, width = C.shape
+    (rows, width), dev = _first(C, "C", _BF16 + _CODES, 2)
+    at = _arg(C, "C", _BF16 + _CODES, (rows, width), dev)
     if C.dtype in _CODES:
-        _tensor(c_scale, "c_scale", (torch.float32,), (rows,), C.device)
-        if rope is not None:
-            _tensor(rope, "rope", _BF16, (rows, ROTARY), C.device)
-        return Cache(rows, width, 0 if rope is None else ROTARY, KDT_FP8, _ptr(C), _ptr(c_scale), _ptr(rope))
+        scale = _arg(c_scale, "c_scale", _F32, (rows,), dev)
+        if rope is None:
+            return Cache(rows, width, 0, KDT_FP8, at, scale, None)
+        return Cache(rows, width, ROTARY, KDT_FP8, at, scale, _arg(rope, "rope", _BF16, (rows, ROTARY), dev))
     if c_scale is not None or rope is not None:
         raise ValueError("c_scale and rope are only for E4M3FN codes (bf16 rows hold their rotary values)")
     dr = ROTARY if width in (128 + ROTARY, LATENT + ROTARY) else 0
-    return Cache(rows, width - dr, dr, KDT_BF16, _ptr(C), None, None)
+    return Cache(rows, width - dr, dr, KDT_BF16, at, None, None)
 
 
 def cache_write(x, slots, C, c_scale=None, rope=None):
@@ -374,65 +403,54 @@ def cache_write(x, slots, C, c_scale=None, rope=None):
     cache, coded if C holds codes; slots outside the cache write nothing. Slots
     inside it must be distinct."""
     c = make_cache(C, c_scale, rope)
-    _tensor(x, "x", _BF16, (None, c.d + c.dr), C.device)
-    _tensor(slots, "slots", (torch.int32,), (x.shape[0],), C.device)
-    with torch.cuda.device(C.device):
-        _check(lib().misa_cache_write(ctypes.byref(c), _ptr(x), x.shape[0], _ptr(slots), _stream()))
+    (n, _), dev = _first(x, "x", _BF16, 2)
+    _on(C.get_device(), lib().misa_cache_write, c, _arg(x, "x", _BF16, (n, c.d + c.dr), C.get_device()), n,
+        _arg(slots, "slots", _I32, (n,), dev))
 
 
 def cache_read(slots, C, c_scale=None, rope=None, out=None):
     """Rows slots (int32 [n]) of the cache as bfloat16 [n, d (+ 64)]; a slot
     outside the cache gives zeros."""
     c = make_cache(C, c_scale, rope)
-    _tensor(slots, "slots", (torch.int32,), (None,), C.device)
-    n = slots.shape[0]
-    with torch.cuda.device(C.device):
-        if out is None:
-            out = torch.empty((n, c.d + c.dr), dtype=torch.bfloat16, device=C.device)
-        else:
-            _tensor(out, "out", _BF16, (n, c.d + c.dr), C.device)
-        _check(lib().misa_cache_read(ctypes.byref(c), _ptr(slots), n, _ptr(out), _stream()))
+    (n,), dev = _first(slots, "slots", _I32, 1)
+    at, width = _arg(slots, "slots", _I32, (n,), C.get_device()), c.d + c.dr
+    if out is None:
+        out = torch.empty((n, width), dtype=torch.bfloat16, device=C.device)
+    _on(dev, lib().misa_cache_read, c, at, n, _arg(out, "out", _BF16, (n, width), dev))
     return out
 
 
 def _attention(call, need, p, q, width, with_lse, ws, out):
     """Output, log-sums and workspace of an attention call, and the call."""
-    T, H, _ = q.shape
-    with torch.cuda.device(q.device):
-        if out is None:
-            out = torch.empty((T, H, width), dtype=torch.bfloat16, device=q.device)
-        else:
-            _tensor(out, "out", _BF16, (T, H, width), q.device)
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if with_lse else None
-        n = need(ctypes.byref(p))
-        if n == 0:  # the call itself reports what is wrong
-            _check(call(ctypes.byref(p), _ptr(out), _ptr(lse), None, 0, _stream()))
-        if ws is None or ws.numel() * ws.element_size() < n:
-            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:
-            _dev(ws, "ws")
-            if ws.device != q.device:
-                raise ValueError(f"ws is on {ws.device}, not on {q.device}")
-        _check(call(ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), n, _stream()))
+    T, H, dev, device = p.T, p.H, q.get_device(), q.device
+    if out is None:
+        out = torch.empty((T, H, width), dtype=torch.bfloat16, device=device)
+    lse = torch.empty((T, H), dtype=torch.float32, device=device) if with_lse else None
+    n = need(p)
+    if ws is not None:
+        _dev(ws, "ws")
+        if ws.get_device() != dev:
+            raise ValueError(f"ws is on GPU {ws.get_device()}, not on GPU {dev}")
+    if ws is None or ws.numel() * ws.element_size() < n:
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    # (n is 0 for a call that the library refuses; the call says why)
+    _on(dev, call, p, _arg(out, "out", _BF16, (T, H, width), dev), lse.data_ptr() if with_lse else None, ws.data_ptr(), n)
     return (out, lse) if with_lse else out
 
 
 def make_latent_problem(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None) -> LatentProblem:
     c = make_cache(C, c_scale, rope)
-    _tensor(q, "q", _BF16, (None, None, LATENT + ROTARY), C.device)
-    T, H, _ = q.shape
+    (T, H, _), dev = _first(q, "q", _BF16, 3)
+    at = _arg(q, "q", _BF16, (T, H, LATENT + ROTARY), C.get_device())
     if (pos is None) == (idx is None):
         raise ValueError("give either pos [T] (every visible key) or idx [T, k] (the keys of a list)")
+    first = None if base is None else _arg(base, "base", _I32, (T,), dev)
     if pos is not None:
-        _tensor(pos, "pos", (torch.int32,), (T,), q.device)
-    else:
-        _tensor(idx, "idx", (torch.int32,), (T, None), q.device)
-        if idx.shape[1] < 1:
-            raise ValueError("idx must have at least one column")
-    if base is not None:
-        _tensor(base, "base", (torch.int32,), (T,), q.device)
-    return LatentProblem(T, H, 0 if idx is None else idx.shape[1], float(sm_scale), _ptr(q), _ptr(idx), _ptr(pos),
-                         _ptr(base), c)
+        return LatentProblem(T, H, 0, sm_scale, at, None, _arg(pos, "pos", _I32, (T,), dev), first, c)
+    (_, k), _ = _first(idx, "idx", _I32, 2)
+    if k < 1:
+        raise ValueError("idx must have at least one column")
+    return LatentProblem(T, H, k, sm_scale, at, _arg(idx, "idx", _I32, (T, k), dev), None, first, c)
 
 
 def latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None, with_lse=False,
@@ -446,19 +464,19 @@ def latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None
 
 
 def make_expanded_problem(q, kv, rope, pos, sm_scale, base=None) -> ExpandedProblem:
-    _tensor(q, "q", _BF16, (None, None, NOPE + ROTARY))
-    T, H, _ = q.shape
-    _tensor(kv, "kv", _BF16, (None, H, NOPE + VALUE), q.device)
-    L = kv.shape[0]
-    if not rope.is_cuda or rope.dtype not in _BF16 or tuple(rope.shape) != (L, ROTARY) or rope.device != q.device:
+    (T, H, _), dev = _first(q, "q", _BF16, 3)
+    at = _arg(q, "q", _BF16, (T, H, NOPE + ROTARY), dev)
+    (L, _, _), _ = _first(kv, "kv", _BF16, 3)
+    kv_at = _arg(kv, "kv", _BF16, (L, H, NOPE + VALUE), dev)
+    if rope is None or not rope.is_cuda or rope.dtype not in _BF16 or rope.shape != (L, ROTARY) or rope.get_device() != dev:
         raise ValueError("rope must be a bfloat16 GPU tensor [L, 64] on q's device")
-    if rope.stride(1) != 1 or (L > 1 and rope.stride(0) < ROTARY):
+    ld, inner = rope.stride()
+    if L == 1:
+        ld = ROTARY
+    if inner != 1 or ld < ROTARY:
         raise ValueError("rope's rows must be contiguous")
-    _tensor(pos, "pos", (torch.int32,), (T,), q.device)
-    if base is not None:
-        _tensor(base, "base", (torch.int32,), (T,), q.device)
-    ld = rope.stride(0) if L > 1 else ROTARY
-    return ExpandedProblem(T, H, L, float(sm_scale), _ptr(q), _ptr(kv), _ptr(rope), ld, _ptr(pos), _ptr(base))
+    return ExpandedProblem(T, H, L, sm_scale, at, kv_at, rope.data_ptr(), ld, _arg(pos, "pos", _I32, (T,), dev),
+                           None if base is None else _arg(base, "base", _I32, (T,), dev))
 
 
 def expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False, ws=None, out=None):

@@ -29,7 +29,11 @@ CFLAGS = [
 
 # per-source flags: the scoring kernels keep MFMA accumulators in VGPRs, so the
 # fused epilogue reads them without a copy out of the accumulation registers
-EXTRA = {"score_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# the attention kernels plan their LDS themselves: private arrays of rare paths
+# stay in private memory
+EXTRA = {"score_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "latent_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"],
+         "expanded_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"]}
 
 
 def _compile(src: str) -> str:

@@ -80,6 +80,8 @@ static misa_status check_expanded(const misa_expanded_problem* p) {
   if (!p) return fail(MISA_ERR_INVALID_ARG, "problem is NULL");
   MISA_TRY(check_sizes(p->T, p->H, p->sm_scale));
   if (p->L < 1) return fail(MISA_ERR_INVALID_ARG, "L = %d must be >= 1", p->L);
+  if (p->H > (1 << 20)) return fail(MISA_ERR_UNSUPPORTED, "H = %d exceeds 2^20 heads", p->H);
+  if (p->rope_ld > (1 << 24)) return fail(MISA_ERR_UNSUPPORTED, "rope_ld = %lld exceeds 2^24", (long long)p->rope_ld);
   if (p->L > (1 << 30)) return fail(MISA_ERR_UNSUPPORTED, "L = %d exceeds 2^30 keys", p->L);
   if (p->rope_ld < kRotary || p->rope_ld % 8 != 0)
     return fail(MISA_ERR_INVALID_ARG, "rope_ld = %lld must be a multiple of 8 and >= 64", (long long)p->rope_ld);

@@ -6,13 +6,13 @@
 //
 // over the keys base[t] .. base[t] + pos[t] of query t.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention_device.h"
 
 namespace misa {
 
-constexpr int kExpRows = 128;            // queries of a workgroup (32 a wave)
 constexpr int kKvRow = 2 * (kNope + kValue);  // bytes of a head's key and value row
 
 // Order of the 16-byte chunks of a key/value row (32 chunks) and of a rotary
@@ -22,16 +22,21 @@ constexpr int kKvRow = 2 * (kNope + kValue);  // bytes of a head's key and value
 __device__ __forceinline__ int swz_kv(int row) { return ((row & 3) << 2) | ((row >> 2) & 3) | (row & 16); }
 __device__ __forceinline__ int swz_rot(int row) { return (row >> 2) & 7; }
 
-// 128 queries of one head and a share of the keys per workgroup; each wave owns
-// 32 queries and walks every key tile (64 keys, shared through LDS). The
+// 32 NW queries of one head and a share of the keys per workgroup of NW waves; each
+// wave owns 32 queries and walks every key tile (64 keys, shared through LDS). The
 // scores are formed transposed (S^T = K Q^T), so a lane holds weights of one
 // query only, its reference and total are lane values, and the weights are the
 // B operand of O^T = V^T P^T as they stand: the order of the keys inside an
 // MFMA's contraction is free, and the transposing LDS reads of V take the same
-// order as the result rows of S^T.
-__global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
+// order as the result rows of S^T. Two waves share a SIMD, so one's softmax runs
+// beside the other's products.
+template <int NW>
+__global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
+  constexpr int kRows = 32 * NW;
   constexpr int kTileBytes = kAttnTile * (kKvRow + 2 * kRotary);
   constexpr int kRope = kAttnTile * kKvRow;
+  constexpr int kMyRows = kAttnTile / NW;                        // tile rows a wave copies
+  constexpr int kKvCopies = kMyRows / 2, kCopies = kKvCopies + kMyRows / 8;
   __shared__ __attribute__((aligned(1024))) unsigned char tile[2][kTileBytes];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -57,7 +62,7 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
     if (s0 < 0 || s1 <= s0) return;
     a = (int)s0, b = (int)s1;
   };
-  const int t = rt * kExpRows + 32 * w + c;
+  const int t = rt * kRows + 32 * w + c;
   int s_lo, s_hi;
   range(t, s_lo, s_hi);
   const uint32_t kBig = 0x7fffffffu;
@@ -68,9 +73,9 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   const int f_lo = (int)wave_max_u32(some ? (uint32_t)s_lo : kBig), f_hi = (int)wave_min_u32((uint32_t)s_hi);
   int g_lo = (int)kBig, g_hi = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kRows / 64; ++i) {
     int a, b;
-    range(rt * kExpRows + 64 * i + lane, a, b);
+    range(rt * kRows + 64 * i + lane, a, b);
     if (b > a) g_lo = min(g_lo, a), g_hi = max(g_hi, b);
   }
   g_lo = (int)wave_min_u32((uint32_t)g_lo);
@@ -79,28 +84,30 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   tile0 = max(tile0, split * p.tiles_per_split);
   tile1 = min(tile1, (split + 1) * p.tiles_per_split);
 
-  const unsigned char* kv = reinterpret_cast<const unsigned char*>(p.kv) + (int64_t)head * kKvRow;
-  const unsigned char* rope = reinterpret_cast<const unsigned char*>(p.rope);
-  const int64_t kv_ld = (int64_t)p.H * kKvRow, rope_ld = p.rope_ld * 2;
+  const uint64_t kv = (uint64_t)(uintptr_t)p.kv + (uint64_t)head * kKvRow, rope = (uint64_t)(uintptr_t)p.rope;
+  const uint32_t kv_ld = (uint32_t)p.H * kKvRow, rope_ld = (uint32_t)p.rope_ld * 2;
   const uint32_t tile_lds = lds_addr(&tile[0][0]);
-  // copies keys 16 w .. 16 w + 15 of tile ti into buffer b; keys past the last
-  // repeat it (they are masked)
-  auto stage = [&](int b, int ti) {
-    const uint32_t dst = tile_lds + b * kTileBytes;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // two rows a copy
-      const int row = 16 * w + 2 * i + h2;
-      const int64_t s = min(ti * kAttnTile + row, p.L - 1);
-      copy16_to_lds(kv + s * kv_ld + ((c ^ swz_kv(row)) * 16), dst + (16 * w + 2 * i) * kKvRow);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // eight rotary rows a copy
-      const int row = 16 * w + 8 * i + (lane >> 3);
-      const int64_t s = min(ti * kAttnTile + row, p.L - 1);
-      copy16_to_lds(rope + s * rope_ld + (((lane & 7) ^ swz_rot(row)) * 16), dst + kRope + (16 * w + 8 * i) * (2 * kRotary));
+  // copy j of the wave's rows of the tile that starts at key k0, to LDS at dst;
+  // keys past the last repeat it (they are masked)
+  auto copy = [&](uint32_t dst, int k0, int j, int ln) {
+    if (j < kKvCopies) {  // two rows a copy
+      const int r0 = kMyRows * w + 2 * j, row = r0 + (ln >> 5);
+      const int sb = min(k0 + r0, p.L - 1);
+      const uint32_t step = sb + 1 < p.L ? kv_ld : 0u;
+      copy16_to_lds_at(reinterpret_cast<const void*>(kv + (uint64_t)(uint32_t)sb * kv_ld),
+                       (ln >= 32 ? step : 0u) + (((ln & 31) ^ swz_kv(row)) * 16), dst + r0 * kKvRow);
+    } else {              // eight rotary rows a copy
+      const int r0 = kMyRows * w + 8 * (j - kKvCopies), row = r0 + (ln >> 3);
+      const int sb = min(k0 + r0, p.L - 1);
+      copy16_to_lds_at(reinterpret_cast<const void*>(rope + (uint64_t)(uint32_t)sb * rope_ld),
+                       (uint32_t)min(ln >> 3, p.L - 1 - sb) * rope_ld + (((ln & 7) ^ swz_rot(row)) * 16),
+                       dst + kRope + r0 * (2 * kRotary));
     }
   };
-  if (tile0 < tile1) stage(0, tile0);
+  if (tile0 < tile1) {
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) copy(tile_lds, tile0 * kAttnTile, j, lane);
+  }
 
   // Q as the B operand: K step ks, lane (query c, half h2): values 16 ks + 8 h2 .. + 7
   const float sm = scale_magnitude(p.sm_log2);
@@ -129,22 +136,20 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
   const uint32_t a_val =
       vrow * kKvRow + (((kNope / 8 + 2 * ((lane >> 4) & 1) + ((lo & 3) >> 1)) ^ swz_kv(vrow)) * 16) + (lo & 1) * 8;
 
-  for (int ti = tile0; ti < tile1; ++ti) {
-    const uint32_t tb = tile_lds + ((ti - tile0) & 1) * kTileBytes;
-    if (ti + 1 < tile1) stage((ti + 1 - tile0) & 1, ti + 1);
+  // one tile; MIXED: not every query of the wave sees every key (or none does)
+  auto step = [&](int ti, auto mixed) {
+    constexpr bool MIXED = decltype(mixed)::value;
+    const uint32_t tb = tile_lds + ((ti - tile0) & 1) * kTileBytes, next_lds = tile_lds + ((ti + 1 - tile0) & 1) * kTileBytes;
     const int k0 = ti * kAttnTile;
-    if (k0 < w_hi && k0 + kAttnTile > w_lo) {
-      // ---- scores of keys 32 n + 8 (e / 4) + 4 h2 + e % 4 (result rows) for query c
-      f32x16 s[2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
-      const uint32_t ka = tb + a_key, ra = tb + a_rot, va = tb + a_val;
+    const int k_next = ti + 1 < tile1 ? k0 + kAttnTile : p.L;  // (no next tile: the last key's row, unused)
+    const int ln = anew(lane);
+    if (!MIXED || (k0 < w_hi && k0 + kAttnTile > w_lo)) {
+      // ---- scores of keys 32 n + 8 (e / 4) + 4 h2 + e % 4 (result rows) for query c.
       // Operand reads run kAhead steps before their products, in one sequence:
       // key rows 32 n + c of K step ks (2 ks + n), then values 32 d .. + 31 of
       // keys 16 i .. + 15 (4 i + d)
-      constexpr int kKeyReads = 24, kAhead = 8;
+      constexpr int kKeyReads = 24, kAhead = 4;
+      const uint32_t ka = tb + a_key, ra = tb + a_rot, va = tb + a_val;
       bf16x8 ring[kAhead];
       auto read = [&](int i) -> bf16x8 {
         if (i < 16) return lds_read<bf16x8>((ka ^ (32 * (i >> 1))) + (i & 1) * 32 * kKvRow);
@@ -153,18 +158,24 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
         const uint32_t at = va ^ (64 * d) ^ (256 * (k & 1));
         return join_rows(lds_read_tr16(at + 16 * k * kKvRow), lds_read_tr16((at ^ 32) + (16 * k + 8) * kKvRow));
       };
+      f32x16 s[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < kKeyReads; ++i) {
         s[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i % kAhead], qf[i >> 1], s[i & 1], 0, 0, 0);
-        ring[i % kAhead] = read(i + kAhead);
+        if (i + kAhead < kKeyReads) ring[i % kAhead] = read(i + kAhead);
+        // the next tile's copies, spread over these products
+        if ((i + 1) * kCopies / kKeyReads != i * kCopies / kKeyReads) copy(next_lds, k_next, i * kCopies / kKeyReads, ln);
         __builtin_amdgcn_sched_barrier(0);
       }
-      const bool mixed = k0 < f_lo || k0 + kAttnTile > f_hi;  // not every query sees every key
-      bool odd = false;                                       // and a value is not finite
-      if (__builtin_expect(mixed, 0)) {
+      bool odd = false;  // a value is not finite
+      if constexpr (MIXED) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -188,81 +199,114 @@ __global__ __launch_bounds__(256, 2) void k_expanded(ExpandedArgs p) {
         for (int d = 0; d < 4; ++d) o[d] *= f;
       }
       bf16x8 pb[4];
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float x = exp2_fast(fmaf(s[n][e], sm, -m));
-          l += x;  // the total keeps 32 bits; the weights are rounded to bf16 for the matrix cores
+          sum[e & 3] += x;  // the total keeps 32 bits; the weights are rounded to bf16 for the matrix cores
           pb[2 * n + (e >> 3)][e & 7] = (__bf16)x;
         }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // ---- sums of values 32 d + (result row) for query c
-      if (__builtin_expect(!odd, 1)) {
+      if (!MIXED || __builtin_expect(!odd, 1)) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ring[i] = read(kKeyReads + i);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(kKeyReads + i) % kAhead], pb[i >> 2], o[i & 3], 0, 0, 0);
-          if (i + kAhead < 16) ring[(kKeyReads + i) % kAhead] = read(kKeyReads + i + kAhead);
+          o[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[i % kAhead], pb[i >> 2], o[i & 3], 0, 0, 0);
+          if (i + kAhead < 16) ring[i % kAhead] = read(kKeyReads + i + kAhead);
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {  // each key with such a value adds it to the queries that see the key
+        f32x16 sums[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const bf16x8 a = read(kKeyReads + 4 * i + d);
+        for (int d = 0; d < 4; ++d) sums[d] = o[d];
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-              const bf16x8 one = part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1);
-              f32x16 z;
+        for (int i = 0; i < 16; ++i) {
+          const bf16x8 a = read(kKeyReads + i);
+          const bf16x8 pi = i < 8 ? (i < 4 ? pb[0] : pb[1]) : (i < 12 ? pb[2] : pb[3]);
+          f32x16 acc = sums[i & 3];
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) {
+            f32x16 z;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) z[e] = 0.f;
-              z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(one, pb[i], z, 0, 0, 0);
-              const int key = k0 + 16 * i + 8 * ((k & 7) >> 2) + 4 * (k >> 3) + (k & 3);
-              if (key >= s_lo && key < s_hi) o[d] += z;
-            }
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part_of<false>(a, 0), pb[i], o[d], 0, 0, 0);
+            for (int e = 0; e < 16; ++e) z[e] = 0.f;
+            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part_of<true>(a, h2 == (k >> 3) ? (k & 7) : -1), pi, z, 0, 0, 0);
+            const int key = k0 + 16 * (i >> 2) + 8 * ((k & 7) >> 2) + 4 * (k >> 3) + (k & 3);
+            if (key >= s_lo && key < s_hi) acc += z;
           }
+          sums[i & 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part_of<false>(a, 0), pi, acc, 0, 0, 0);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = sums[d];
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy(next_lds, k_next, j, ln);
     }
     wait_copies();
     lds_barrier();
+  };
+  for (int ti = tile0; ti < tile1; ++ti) {
+    for (; ti < tile1 && ti * kAttnTile >= f_lo && (ti + 1) * kAttnTile <= f_hi; ++ti) step(ti, std::false_type{});
+    if (ti < tile1) step(ti, std::true_type{});
   }
 
-  // ---- result: lane holds values 32 d + 8 i + 4 h2 + 0..3 of query c
+  // ---- result, through LDS (the wave's own 8 KB) so that rows leave in whole lines:
+  // 256 bytes of each of 32 rows at a time, chunks in an order that depends on the row
   const float tot = sum_halves(l);
-  if (t >= p.T) return;
-  const int64_t R = (int64_t)t * p.H + head;
+  const uint32_t mine = tile_lds + w * 32 * 256;
+  const int rows_here = min(32, p.T - (rt * kRows + 32 * w));
+  const int64_t R0 = (int64_t)(rt * kRows + 32 * w) * p.H + head;
+  auto put = [&](unsigned char* dst, int64_t stride) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int rr = 4 * i + (lane >> 4);
+      const u32x4 v = lds_read<u32x4>(mine + rr * 256 + ((lo ^ (rr & 15)) * 16));
+      if (rr < rows_here) *reinterpret_cast<u32x4*>(dst + rr * stride + lo * 16) = v;
+    }
+  };
   if (p.splits > 1) {
-    const int64_t pr = (int64_t)split * p.T * p.H + R;
-    float* po = p.part + pr * kValue + 4 * h2;
+    const int64_t pr = (int64_t)split * p.T * p.H + R0;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d0 = 0; d0 < 4; d0 += 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * i) =
-            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-    if (h2 == 0) p.part_ml[pr * 2] = m, p.part_ml[pr * 2 + 1] = tot;
+      for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(mine + c * 256 + (((8 * d + 2 * i + h2) ^ (c & 15)) * 16)) =
+              f32x4{o[d0 + d][4 * i], o[d0 + d][4 * i + 1], o[d0 + d][4 * i + 2], o[d0 + d][4 * i + 3]};
+      put(reinterpret_cast<unsigned char*>(p.part + pr * kValue + 32 * d0), (int64_t)p.H * kValue * 4);
+    }
+    if (c < rows_here && h2 == 0) {
+      p.part_ml[(pr + (int64_t)c * p.H) * 2] = m;
+      p.part_ml[(pr + (int64_t)c * p.H) * 2 + 1] = tot;
+    }
   } else {
     const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
-    uint16_t* po = p.out + R * kValue + 4 * h2;
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f32x4 v = {o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
-        *reinterpret_cast<bf16x4*>(po + 32 * d + 8 * i) = __builtin_convertvector(v, bf16x4);
+        *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(mine + c * 256 + (((4 * d + i) ^ (c & 15)) * 16) + h2 * 8) =
+            __builtin_convertvector(v, bf16x4);
       }
-    if (p.lse && h2 == 0) p.lse[R] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
+    put(reinterpret_cast<unsigned char*>(p.out + R0 * kValue), (int64_t)p.H * kValue * 2);
+    if (p.lse && c < rows_here && h2 == 0)
+      p.lse[R0 + (int64_t)c * p.H] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
   }
 }
 
 AttnPlan expanded_plan(int T, int H, int L) {
   AttnPlan pl{};
-  pl.nq = kExpRows;
-  pl.row_tiles = (T + kExpRows - 1) / kExpRows;
+  pl.nq = T > 128 ? 256 : 128;
+  pl.row_tiles = (T + pl.nq - 1) / pl.nq;
   const int tiles = std::max(1, (L + kAttnTile - 1) / kAttnTile);
   const int64_t wgs = std::max<int64_t>(1, (int64_t)pl.row_tiles * H);
-  const int want = (int)std::max<int64_t>(1, 512 / wgs);
+  const int want = (int)std::max<int64_t>(1, (pl.nq == 256 ? 256 : 512) / wgs);
   pl.tiles_per_split = (tiles + std::min(want, tiles) - 1) / std::min(want, tiles);
   pl.splits = (tiles + pl.tiles_per_split - 1) / pl.tiles_per_split;
   return pl;
@@ -282,7 +326,9 @@ hipError_t launch_expanded(const LaunchCtx& cx, ExpandedArgs a, const AttnPlan& 
     a.part_ml = a.part + rows * pl.splits * kValue;
   }
   const int64_t n = (int64_t)pl.row_tiles * pl.splits * a.H;
-  const hipError_t e = cx.launch("k_expanded", k_expanded, dim3((unsigned)((n + 7) / 8 * 8)), dim3(256), 0, a);
+  const dim3 grid((unsigned)((n + 7) / 8 * 8));
+  const hipError_t e = pl.nq == 256 ? cx.launch("k_expanded", k_expanded<8>, grid, dim3(512), 0, a)
+                                    : cx.launch("k_expanded", k_expanded<4>, grid, dim3(256), 0, a);
   if (e != hipSuccess || pl.splits <= 1) return e;
   return launch_join(cx, a.part, a.part_ml, pl.splits, rows, kValue, a.out, a.lse);
 }
