@@ -53,6 +53,7 @@ static CacheArgs cache_args(const misa_cache* c, int32_t n, const int32_t* slots
 static misa_status check_sizes(int32_t T, int32_t H, float sm_scale) {
   if (T < 0) return fail(MISA_ERR_INVALID_ARG, "T = %d is negative", T);
   if (H < 1) return fail(MISA_ERR_INVALID_ARG, "H = %d must be >= 1", H);
+  if (T > (1 << 22)) return fail(MISA_ERR_UNSUPPORTED, "T = %d exceeds 2^22 queries", T);
   if ((int64_t)T * H > kMaxRows) return fail(MISA_ERR_UNSUPPORTED, "T * H = %lld exceeds 2^30", (long long)T * H);
   if (!std::isfinite(sm_scale)) return fail(MISA_ERR_INVALID_ARG, "sm_scale is not finite");
   return MISA_OK;
@@ -72,8 +73,7 @@ static misa_status check_latent(const misa_latent_problem* p) {
 
 static AttnPlan plan_of(const misa_latent_problem* p) {
   const bool lists = p->idx != nullptr;
-  return latent_plan(p->T, p->H, lists ? p->k : p->cache.rows, lists, p->cache.dtype == MISA_K_FP8_E4M3FN,
-                     !lists && !p->base);
+  return latent_plan(p->T, p->H, lists ? p->k : p->cache.rows, !lists && !p->base);
 }
 
 static misa_status check_expanded(const misa_expanded_problem* p) {
@@ -105,6 +105,7 @@ extern "C" {
 misa_status misa_cache_write(const misa_cache* cache, const void* x, int32_t n, const int32_t* slots, void* stream) {
   MISA_TRY(check_cache(cache));
   if (n < 0) return fail(MISA_ERR_INVALID_ARG, "n = %d is negative", n);
+  if (n > (1 << 25)) return fail(MISA_ERR_UNSUPPORTED, "n = %d exceeds 2^25 rows", n);
   if (n == 0) return MISA_OK;
   MISA_TRY(check_ptr(x, "x", 16));
   MISA_TRY(check_ptr(slots, "slots", 4));
@@ -118,6 +119,7 @@ misa_status misa_cache_write(const misa_cache* cache, const void* x, int32_t n, 
 misa_status misa_cache_read(const misa_cache* cache, const int32_t* slots, int32_t n, void* out, void* stream) {
   MISA_TRY(check_cache(cache));
   if (n < 0) return fail(MISA_ERR_INVALID_ARG, "n = %d is negative", n);
+  if (n > (1 << 25)) return fail(MISA_ERR_UNSUPPORTED, "n = %d exceeds 2^25 rows", n);
   if (n == 0) return MISA_OK;
   MISA_TRY(check_ptr(out, "out", 16));
   MISA_TRY(check_ptr(slots, "slots", 4));

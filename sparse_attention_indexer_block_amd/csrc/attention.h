@@ -43,7 +43,7 @@ struct LatentArgs {
   // set by the launcher
   float* part;           // [splits, T * H, 512] partial sums
   float* part_ml;        // [splits, T * H, 2] their reference and weight
-  int32_t splits, tiles_per_split;
+  int32_t splits;
   int32_t head_tiles;    // row tiles per query (rows of one query), 0: tiles run over all T * H rows
   int32_t row_tiles;
 };
@@ -51,7 +51,7 @@ struct LatentArgs {
 struct AttnPlan {
   int nq, head_tiles, row_tiles, splits, tiles_per_split;
 };
-AttnPlan latent_plan(int T, int H, int keys, bool lists, bool fp8, bool shared_keys);
+AttnPlan latent_plan(int T, int H, int keys, bool shared_keys);
 size_t latent_ws_bytes(const AttnPlan& pl, int T, int H);
 hipError_t launch_latent(const LaunchCtx& cx, LatentArgs a, const AttnPlan& pl, bool fp8, void* ws);
 
@@ -69,7 +69,7 @@ struct ExpandedArgs {
   float* lse;            // [T, H] or null
   float* part;           // [splits, T * H, 128]
   float* part_ml;        // [splits, T * H, 2]
-  int32_t splits, tiles_per_split;
+  int32_t splits;
   int32_t row_tiles;
 };
 AttnPlan expanded_plan(int T, int H, int L);

@@ -16,10 +16,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // score (-inf) minus it is -inf and weighs 0, and below every score.
 constexpr float kNoMax = -3.0e38f;
 // A row's reference is raised when a score passes it by this much (in powers
-// of two): weights stay below 2^8 and the accumulated sums are rescaled in few
-// tiles only. The reference cancels in the quotient, so results do not change
-// beyond fp32 rounding.
-constexpr float kSlack = 8.0f;
+// of two): weights stay below 2^32, far inside fp32 and bf16, and the
+// accumulated sums are rescaled in hardly any tile but the first (with 2^8 one
+// of 32 rows passed it every few tiles). The reference cancels in the quotient,
+// so results do not change beyond fp32 rounding.
+constexpr float kSlack = 32.0f;
 
 // Starts a copy of 16 bytes a lane from global memory to LDS at lds + 16 * lane
 // (lds: wave-uniform byte address). It counts in vmcnt and is waited for with
@@ -49,7 +50,6 @@ __device__ __forceinline__ void copy16_to_lds_at(const void* base, uint32_t off,
       : "memory");
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
 // Workgroup barrier that waits for this wave's LDS accesses only (copies to
 // LDS stay in flight).
 __device__ __forceinline__ void lds_barrier() {

@@ -43,15 +43,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h2 = lane >> 5, lo = lane & 15;
 
-  // each XCD takes a run of (head, split, row tile): the row tiles of a head
-  // share its keys; the last row tiles, with the most keys under a causal mask, first
+  // each XCD takes a run of (split, head, row tile): the row tiles of a head
+  // share its keys, the heads of a split the rows that hold them side by side;
+  // the last row tiles, with the most keys under a causal mask, first
   const int per = (int)(gridDim.x / 8);
   const int lid = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-  const int head = lid / (p.row_tiles * p.splits);
-  if (head >= p.H) return;
-  const int rem = lid % (p.row_tiles * p.splits);
-  const int split = rem % p.splits;
-  const int rt = p.row_tiles - 1 - rem / p.splits;
+  const int rt = p.row_tiles - 1 - lid % p.row_tiles;
+  const int head = lid / p.row_tiles % p.H, split = lid / p.row_tiles / p.H;
+  if (split >= p.splits) return;
 
   // ---- key ranges: of the lane's query, of the wave and of the workgroup
   auto range = [&](int t, int& a, int& b) {
@@ -69,8 +68,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   const bool some = s_hi > s_lo;
   const int w_lo = (int)wave_min_u32(some ? (uint32_t)s_lo : kBig);    // the wave's first key
   const int w_hi = (int)wave_max_u32((uint32_t)s_hi);                  // and end
-  // keys that every query of the wave sees (none if one sees none)
-  const int f_lo = (int)wave_max_u32(some ? (uint32_t)s_lo : kBig), f_hi = (int)wave_min_u32((uint32_t)s_hi);
+  // keys that every query of the wave sees; a query that sees none is set to its
+  // result at the end, whatever it gathers
+  const int f_lo = (int)wave_max_u32(some ? (uint32_t)s_lo : 0u);
+  const int f_hi = w_hi == 0 ? 0 : (int)wave_min_u32(some ? (uint32_t)s_hi : kBig);
   int g_lo = (int)kBig, g_hi = 0;
 #pragma unroll
   for (int i = 0; i < kRows / 64; ++i) {
@@ -80,9 +81,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   }
   g_lo = (int)wave_min_u32((uint32_t)g_lo);
   g_hi = (int)wave_max_u32((uint32_t)g_hi);
-  int tile0 = g_lo / kAttnTile, tile1 = (g_hi + kAttnTile - 1) / kAttnTile;
-  tile0 = max(tile0, split * p.tiles_per_split);
-  tile1 = min(tile1, (split + 1) * p.tiles_per_split);
+  int tile0 = min(g_lo, g_hi) / kAttnTile, tile1 = (g_hi + kAttnTile - 1) / kAttnTile;
+  // an equal share of the tiles that this row tile has
+  const int share = (max(tile1 - tile0, 0) + p.splits - 1) / p.splits;
+  tile0 += split * share;
+  tile1 = min(tile1, tile0 + share);
 
   const uint64_t kv = (uint64_t)(uintptr_t)p.kv + (uint64_t)head * kKvRow, rope = (uint64_t)(uintptr_t)p.rope;
   const uint32_t kv_ld = (uint32_t)p.H * kKvRow, rope_ld = (uint32_t)p.rope_ld * 2;
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
             const int key = k0 + 32 * n + 8 * (e >> 2) + 4 * h2 + (e & 3);
             s[n][e] = key >= s_lo && key < s_hi ? s[n][e] : -INFINITY;
           }
-#pragma unroll 1
+#pragma unroll 4
         for (int i = 0; i < 16; ++i) odd |= any_odd(read(kKeyReads + i));
         odd = __any(odd);
       }
@@ -256,6 +259,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
 
   // ---- result, through LDS (the wave's own 8 KB) so that rows leave in whole lines:
   // 256 bytes of each of 32 rows at a time, chunks in an order that depends on the row
+  if (!some) {
+    m = kNoMax;
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+  }
   const float tot = sum_halves(l);
   const uint32_t mine = tile_lds + w * 32 * 256;
   const int rows_here = min(32, p.T - (rt * kRows + 32 * w));
@@ -300,16 +311,33 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   }
 }
 
+// Queries per workgroup and splits of the keys, by what they cost on this card, in
+// us: 128 queries take 1.65 a tile with four waves and 256 take 3.1 with eight (1.85 and 2.2
+// alone on its compute unit), a workgroup starts and ends in 9, and partial sums
+// (512 bytes a row and split) are written and joined at 5 TB/s after 4 of launch.
+// The queries are taken to be the last of the keys, which is the most work.
+// Measured (4 / 8 waves): 100 queries over 32768 keys, 16 heads, 60 / 64; 2048 and
+// 8192 causal ones 63 / 77 and 432 / 408.
 AttnPlan expanded_plan(int T, int H, int L) {
-  AttnPlan pl{};
-  pl.nq = T > 128 ? 256 : 128;
-  pl.row_tiles = (T + pl.nq - 1) / pl.nq;
-  const int tiles = std::max(1, (L + kAttnTile - 1) / kAttnTile);
-  const int64_t wgs = std::max<int64_t>(1, (int64_t)pl.row_tiles * H);
-  const int want = (int)std::max<int64_t>(1, (pl.nq == 256 ? 256 : 512) / wgs);
-  pl.tiles_per_split = (tiles + std::min(want, tiles) - 1) / std::min(want, tiles);
-  pl.splits = (tiles + pl.tiles_per_split - 1) / pl.tiles_per_split;
-  return pl;
+  const double tiles = std::max(1, (L + kAttnTile - 1) / kAttnTile);
+  const double mean = std::max(tiles - T / (2.0 * kAttnTile), 0.5 * tiles);
+  AttnPlan best{};
+  double least = 0.0;
+  for (int nq = 128; nq <= 256; nq += 128) {
+    AttnPlan pl{};
+    pl.nq = nq;
+    pl.row_tiles = (T + nq - 1) / nq;
+    const double wgs = (double)pl.row_tiles * H;
+    const int most = (int)std::max(1.0, std::min((nq == 256 ? 256 : 512) / wgs, tiles));
+    for (int s = 1;; s = std::min(2 * s, most)) {
+      pl.splits = s;
+      const double all = wgs * mean * (nq == 256 ? 3.1 : 1.65) / 256, longest = tiles / s * (nq == 256 ? 2.2 : 1.85);
+      const double cost = std::max(all, longest) + 9.0 + (s > 1 ? 4.0 + 1.0 * s * T * (double)H * (kValue * 4) / 5.0e6 : 0.0);
+      if (best.nq == 0 || cost < least) best = pl, least = cost;
+      if (s == most) break;
+    }
+  }
+  return best;
 }
 
 size_t expanded_ws_bytes(const AttnPlan& pl, int T, int H) {
@@ -319,7 +347,6 @@ size_t expanded_ws_bytes(const AttnPlan& pl, int T, int H) {
 hipError_t launch_expanded(const LaunchCtx& cx, ExpandedArgs a, const AttnPlan& pl, void* ws) {
   const int64_t rows = (int64_t)a.T * a.H;
   a.splits = pl.splits;
-  a.tiles_per_split = pl.tiles_per_split;
   a.row_tiles = pl.row_tiles;
   if (pl.splits > 1) {
     a.part = static_cast<float*>(ws);

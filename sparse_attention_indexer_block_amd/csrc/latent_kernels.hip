@@ -110,8 +110,10 @@ struct LatentWork {
     }
     j1 = __builtin_amdgcn_readfirstlane(j1);
     same = __builtin_amdgcn_readfirstlane(same);
-    tile_end = min((j1 + kAttnTile - 1) / kAttnTile, (split + 1) * p.tiles_per_split);
-    cur = split * p.tiles_per_split;
+    // an equal share of the tiles that there are here
+    const int tiles = (j1 + kAttnTile - 1) / kAttnTile, share = (tiles + p.splits - 1) / p.splits;
+    cur = split * share;
+    tile_end = min(tiles, cur + share);
   }
   __device__ __forceinline__ int left() const { return base < 0 ? 0 : max(0, p.rows - base); }
   // keys of tile ti (bits) that a unit with limit lim sees, of those that the tile holds
@@ -119,19 +121,18 @@ struct LatentWork {
     const int n = lim - ti * kAttnTile;
     return n >= kAttnTile ? held : n <= 0 ? 0 : held & ((1ull << n) - 1);
   }
-  // entry 64 * ti + lane of the list
+  // entry 64 * ti + lane of the list (the last one past its end; row_of knows).
+  // A load without a branch: it is asked for a tile ahead, and a branch around
+  // it would wait for what is in flight.
   __device__ __forceinline__ int list_entry(int ti) const {
-    if constexpr (LIST) {
-      const int j = ti * kAttnTile + lane;
-      if (j < p.k) return p.idx[(int64_t)t * p.k + j];
-    }
+    if constexpr (LIST) return p.idx[(int64_t)t * p.k + min(ti * kAttnTile + lane, p.k - 1)];
     return -1;
   }
   // the cache row of key 64 * ti + lane, or -1; v: its list entry
   __device__ __forceinline__ int row_of(int ti, int v) const {
     if constexpr (LIST) {
       const int64_t row = (int64_t)v + base;
-      return (v >= 0 && base >= 0 && row < p.rows) ? (int)row : -1;
+      return (v >= 0 && base >= 0 && row < p.rows && ti * kAttnTile + lane < p.k) ? (int)row : -1;
     } else {
       const int j = ti * kAttnTile + lane;
       return j < j1 ? base + j : -1;
@@ -265,14 +266,15 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   const uint32_t tile_lds = lds_addr(&tile[0][0]);
   TileCopy<Tile, FP8> copies{p, w, lane};
   auto key_scale = [&](int rows) -> float {
-    if constexpr (FP8) return rows >= 0 ? p.scale[rows] : 0.f;
+    if constexpr (FP8) return p.scale[max(rows, 0)];  // (what a row that is no key is scaled by is dropped)
     return 0.f;
   };
 
   int rows_cur, rows_nxt;
-  int cur = wk.find_tile(wk.cur, wk.list_entry(wk.cur), rows_cur);
-  int nxt = wk.find_tile(cur + 1, wk.list_entry(cur + 1), rows_nxt);
-  float sc_cur = key_scale(rows_cur);
+  const int v0 = wk.list_entry(wk.cur), v1 = wk.list_entry(wk.cur + 1);
+  int cur = wk.find_tile(wk.cur, v0, rows_cur);
+  int nxt = wk.find_tile(cur + 1, cur == wk.cur ? v1 : wk.list_entry(cur + 1), rows_nxt);
+  float sc_cur = rows_cur >= 0 ? key_scale(rows_cur) : 0.f;
   copies.aim(rows_cur);
   if (cur < tile_end) copies.all(tile_lds);
   copies.aim(rows_nxt);
@@ -465,8 +467,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
     wait_copies();
     lds_barrier();
     cur = nxt;
+    sc_cur = rows_nxt >= 0 ? sc_nxt : 0.f;
     rows_cur = rows_nxt;
-    sc_cur = sc_nxt;
     nxt = wk.find_tile(nxt + 1, v_nn, rows_nxt);
     copies.aim(rows_nxt);
     ++it;
@@ -522,7 +524,7 @@ template <int G, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   using Tile = LatentTile<FP8, true>;
   constexpr int NQ = 32 * G, NS = G / 2;  // rows; 32-key steps of a wave per tile
-  constexpr int kAhead = 6;               // LDS reads in flight
+  constexpr int kAhead = FP8 ? 4 : G == 2 && !LIST ? 5 : 6;  // LDS reads in flight: as many as the registers hold
   __shared__ __attribute__((aligned(1024))) unsigned char tile[2][Tile::kBytes];
   __shared__ __attribute__((aligned(16))) float ksc[2][kAttnTile];
 
@@ -540,7 +542,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   const uint32_t tile_lds = lds_addr(&tile[0][0]);
   TileCopy<Tile, FP8> copies{p, w, lane};
   auto key_scale = [&](int rows) -> float {
-    if constexpr (FP8) return w == 0 && rows >= 0 ? p.scale[rows] : 0.f;
+    if constexpr (FP8) return p.scale[max(rows, 0)];
     return 0.f;
   };
 
@@ -587,9 +589,10 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   auto after = [&](int ti, int who) { return who < 0 ? ti + 1 : ti; };
   int rows_cur, rows_nxt;
   int who_cur, who_nxt;
-  int cur = next_pass(wk.cur, -1, wk.list_entry(wk.cur), who_cur, rows_cur);
-  int nxt = next_pass(after(cur, who_cur), who_cur, wk.list_entry(cur + 1), who_nxt, rows_nxt);
-  if (FP8 && w == 0) ksc[0][lane] = key_scale(rows_cur);
+  const int v0 = wk.list_entry(wk.cur), v1 = wk.list_entry(wk.cur + 1);
+  int cur = next_pass(wk.cur, -1, v0, who_cur, rows_cur);
+  int nxt = next_pass(after(cur, who_cur), who_cur, cur == wk.cur ? v1 : wk.list_entry(cur + 1), who_nxt, rows_nxt);
+  if (FP8 && w == 0) ksc[0][lane] = rows_cur >= 0 ? key_scale(rows_cur) : 0.f;
 
   // Q as the B operand: K step ks, lane (row c, half h2): values 16 ks + 8 h2 .. + 7; with
   // codes, whose 16-byte chunk covers two K steps, 32 (ks / 2) + 16 h2 + 8 (ks % 2) .. + 7.
@@ -743,13 +746,16 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
         const float mm = fmaxf(m, top), f = exp2_fast(m - mm);
+        const bool begun = __any(m > kNoMax);  // (before the first key the sums are zero)
         m = mm;
         l *= f;
+        if (begun) {
 #pragma unroll
         for (int d = 0; d < 16; ++d) {
           in_agprs(o[d]);
           o[d] *= f;
           in_agprs(o[d]);
+        }
         }
       }
       bf16x8 pb[2];
@@ -771,7 +777,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       }
     }
     wait_copies();
-    if (FP8 && w == 0) ksc[(it + 1) & 1][lane] = sc_nxt;
+    if (FP8 && w == 0) ksc[(it + 1) & 1][lane] = rows_nxt >= 0 ? sc_nxt : 0.f;  // (no key: zeros, scaled by none)
     lds_barrier();
     cur = nxt;
     rows_cur = rows_nxt;
@@ -874,20 +880,22 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
 }
 
 // Joins the splits of a row: each split's sums and total weigh 2^(its reference
-// - the largest). One workgroup a row, `width` / 4 threads wide; the threads
-// beyond take further splits and are added through LDS in a fixed order.
-template <int WIDTH>
+// - the largest). WIDTH / 4 threads hold a row; SG such groups take the splits in
+// turn and are added through LDS in a fixed order, and the rest of the workgroup
+// takes further rows.
+template <int WIDTH, int SG>
 __global__ __launch_bounds__(256) void k_join(const float* part, const float* part_ml, int splits, int64_t rows,
                                               uint16_t* out, float* lse) {
-  constexpr int TPR = WIDTH / 4, SG = 256 / TPR;
-  __shared__ __attribute__((aligned(16))) float sums[SG][WIDTH];
-  __shared__ float tots[SG];
-  const int64_t r = blockIdx.x;
-  const int c = threadIdx.x % TPR, sg = threadIdx.x / TPR;
+  constexpr int TPR = WIDTH / 4, ROWS = 256 / TPR / SG;
+  __shared__ __attribute__((aligned(16))) float sums[ROWS][SG][WIDTH];
+  __shared__ float tots[ROWS][SG];
+  const int c = threadIdx.x % TPR, sg = threadIdx.x / TPR % SG, rr = threadIdx.x / TPR / SG;
+  const int64_t r = min((int64_t)blockIdx.x * ROWS + rr, rows - 1);
+  const bool mine = (int64_t)blockIdx.x * ROWS + rr < rows;
   float top = kNoMax;
-  for (int s = threadIdx.x & 63; s < splits; s += 64) top = fmaxf(top, part_ml[((int64_t)s * rows + r) * 2]);
+  for (int s = threadIdx.x & 31; s < splits; s += 32) top = fmaxf(top, part_ml[((int64_t)s * rows + r) * 2]);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));  // (32 lanes share a row)
   float tot = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
@@ -897,42 +905,80 @@ __global__ __launch_bounds__(256) void k_join(const float* part, const float* pa
     tot += f * ml[1];
     acc += *reinterpret_cast<const f32x4*>(part + ((int64_t)s * rows + r) * WIDTH + c * 4) * f;
   }
-  *reinterpret_cast<f32x4*>(&sums[sg][c * 4]) = acc;
-  if (c == 0) tots[sg] = tot;
-  __syncthreads();
-  if (sg != 0) return;
+  if constexpr (SG > 1) {
+    *reinterpret_cast<f32x4*>(&sums[rr][sg][c * 4]) = acc;
+    if (c == 0) tots[rr][sg] = tot;
+    __syncthreads();
+    if (sg != 0) return;
 #pragma unroll
-  for (int i = 1; i < SG; ++i) {
-    acc += *reinterpret_cast<const f32x4*>(&sums[i][c * 4]);
-    tot += tots[i];
+    for (int i = 1; i < SG; ++i) {
+      acc += *reinterpret_cast<const f32x4*>(&sums[rr][i][c * 4]);
+      tot += tots[rr][i];
+    }
   }
+  if (!mine) return;
   const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);
   *reinterpret_cast<bf16x4*>(out + r * WIDTH + c * 4) = __builtin_convertvector(acc * inv, bf16x4);
   if (lse && c == 0) lse[r] = tot == 0.f ? -INFINITY : (top + log2_fast(tot)) * 0.6931471805599453f;
 }
 
+template <int WIDTH, int SG>
+static hipError_t join_as(const LaunchCtx& cx, const float* part, const float* part_ml, int splits, int64_t rows,
+                          uint16_t* out, float* lse) {
+  constexpr int ROWS = 256 / (WIDTH / 4) / SG;
+  return cx.launch("k_join", k_join<WIDTH, SG>, dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(256), 0, part, part_ml,
+                   splits, rows, out, lse);
+}
+
+// Several groups a row where a row has many splits or there are few rows to fill the card with.
 hipError_t launch_join(const LaunchCtx& cx, const float* part, const float* part_ml, int splits, int64_t rows,
                        int width, uint16_t* out, float* lse) {
-  const dim3 grid((unsigned)rows);
-  return width == kLatent
-             ? cx.launch("k_join", k_join<kLatent>, grid, dim3(256), 0, part, part_ml, splits, rows, out, lse)
-             : cx.launch("k_join", k_join<kValue>, grid, dim3(256), 0, part, part_ml, splits, rows, out, lse);
+  if (width == kLatent)
+    return splits > 8 || rows < 1024 ? join_as<kLatent, 2>(cx, part, part_ml, splits, rows, out, lse)
+                                     : join_as<kLatent, 1>(cx, part, part_ml, splits, rows, out, lse);
+  return splits > 8 || rows < 1024 ? join_as<kValue, 8>(cx, part, part_ml, splits, rows, out, lse)
+                                   : join_as<kValue, 1>(cx, part, part_ml, splits, rows, out, lse);
 }
 
 static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-AttnPlan latent_plan(int T, int H, int keys, bool lists, bool fp8, bool shared_keys) {
-  AttnPlan pl{};
-  // units of queries that read the same keys share a tile
-  const int64_t rows16 = (int64_t)cdiv(H, 16) * 16 * (shared_keys ? T : 1), rows32 = (int64_t)cdiv(H, 32) * 32 * (shared_keys ? T : 1);
-  pl.nq = rows16 <= 16 ? 16 : rows16 <= 32 ? 32 : rows32 <= 64 ? 64 : 128;
-  pl.head_tiles = shared_keys ? 0 : cdiv(H, pl.nq);
-  pl.row_tiles = shared_keys ? cdiv(pl.nq <= 32 ? rows16 : rows32, pl.nq) : T * pl.head_tiles;
+// Rows per workgroup and splits of the keys: the cheapest of four widths by what
+// they cost on this card, in us. A workgroup starts and ends in `fixed`, a tile
+// of 64 keys takes `tile` (more rows amortise the gather of a tile, fewer leave
+// less to write where the keys are split), 256 run at a time, and partial sums
+// (2 KB a row and split) are written and joined at 5 TB/s after 4 us of launch.
+// Measured against it, lists of 2048 coded keys, 128 heads (16 / 32 / 64 / 128 rows):
+// 8 queries 32 / 33 / 35 / 38 us, 32 queries 77 / 59 / 51 / 53, 256 queries
+// 577 / 344 / 210 / 174, 1024 queries 2307 / 1371 / 803 / 670.
+AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
+  struct Width {
+    int rows, unit;
+    double fixed, tile;
+  };
+  static const Width widths[] = {{16, 16, 8.0, 2.25}, {32, 16, 11.0, 2.7}, {64, 32, 15.0, 3.15}, {128, 32, 20.0, 5.2}};
   const int tiles = std::max(1, cdiv(keys, kAttnTile));
-  const int want = std::max(1, 256 / std::max(1, pl.row_tiles));
-  pl.tiles_per_split = std::max(1, cdiv(tiles, std::min(want, tiles)));
-  pl.splits = cdiv(tiles, pl.tiles_per_split);
-  return pl;
+  AttnPlan best{};
+  double least = 0.0;
+  for (const Width& w : widths) {
+    AttnPlan pl{};
+    pl.nq = w.rows;
+    // units of queries that read the same keys share a tile
+    pl.head_tiles = shared_keys ? 0 : cdiv(H, w.rows);
+    const int64_t row_tiles = shared_keys ? ((int64_t)cdiv(H, w.unit) * w.unit * T + w.rows - 1) / w.rows
+                                          : (int64_t)T * pl.head_tiles;
+    pl.row_tiles = (int)row_tiles;
+    const int most = (int)std::max<int64_t>(1, std::min<int64_t>(256 / row_tiles, tiles));
+    for (int want = 1;; want = std::min(2 * want, most)) {
+      pl.tiles_per_split = cdiv(tiles, want);
+      pl.splits = cdiv(tiles, pl.tiles_per_split);
+      const double rounds = (double)((row_tiles * pl.splits + 255) / 256);
+      double cost = rounds * (w.fixed + pl.tiles_per_split * w.tile);
+      if (pl.splits > 1) cost += 4.0 + (double)pl.splits * T * H * (kLatent * 4) / 5.0e6;
+      if (best.nq == 0 || cost < least) best = pl, least = cost;
+      if (want == most) break;
+    }
+  }
+  return best;
 }
 
 size_t latent_ws_bytes(const AttnPlan& pl, int T, int H) {
@@ -966,7 +1012,6 @@ static hipError_t launch_latent_t(const LaunchCtx& cx, const LatentArgs& a, int 
 hipError_t launch_latent(const LaunchCtx& cx, LatentArgs a, const AttnPlan& pl, bool fp8, void* ws) {
   const int64_t rows = (int64_t)a.T * a.H;
   a.splits = pl.splits;
-  a.tiles_per_split = pl.tiles_per_split;
   a.head_tiles = pl.head_tiles;
   a.row_tiles = pl.row_tiles;
   if (pl.splits > 1) {
