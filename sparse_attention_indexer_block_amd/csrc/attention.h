@@ -49,7 +49,7 @@ struct LatentArgs {
 };
 // How a call is cut: rows per workgroup and splits of the key axis.
 struct AttnPlan {
-  int nq, head_tiles, row_tiles, splits, tiles_per_split;
+  int nq, head_tiles, row_tiles, splits;
 };
 AttnPlan latent_plan(int T, int H, int keys, bool shared_keys);
 size_t latent_ws_bytes(const AttnPlan& pl, int T, int H);

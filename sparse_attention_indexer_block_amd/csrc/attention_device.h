@@ -104,8 +104,10 @@ __device__ __forceinline__ bf16x8 join_rows(s16x4 a, s16x4 b) {
 }
 
 // The softmax scale as the kernels use it: positive (queries change sign with
-// it) and not zero (the smallest scale weighs every key alike).
-__device__ __forceinline__ float scale_magnitude(float sm_log2) { return fmaxf(fabsf(sm_log2), 1e-37f); }
+// it) and not zero, so that a masked score (-inf) times it stays -inf. The
+// smallest number, 2^-149, weighs all finite scores (below 2^128) alike to
+// within 2^-21, as a scale of zero does.
+__device__ __forceinline__ float scale_magnitude(float sm_log2) { return fmaxf(fabsf(sm_log2), 0x1p-149f); }
 __device__ __forceinline__ bf16x8 flip_sign(bf16x8 a, uint32_t mask) {
   u32x4 v = __builtin_bit_cast(u32x4, a);
   v ^= mask;
@@ -121,9 +123,6 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(u32x2 v) {
   r.w = fp8x2_to_bf16x2<true>(v.y);
   return __builtin_bit_cast(bf16x8, r);
 }
-
-// (The sums of such a tile go through thread-private memory, which lets the
-// rare path be a loop: it costs the common one no registers.)
 
 // Keys 0 .. pos of a prefix of `left` keys (0 for pos < 0).
 __device__ __forceinline__ int visible_keys(int pos, int left) { return pos < 0 ? 0 : (pos < left ? pos + 1 : left); }

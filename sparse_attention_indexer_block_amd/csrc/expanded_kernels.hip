@@ -28,8 +28,7 @@ __device__ __forceinline__ int swz_rot(int row) { return (row >> 2) & 7; }
 // query only, its reference and total are lane values, and the weights are the
 // B operand of O^T = V^T P^T as they stand: the order of the keys inside an
 // MFMA's contraction is free, and the transposing LDS reads of V take the same
-// order as the result rows of S^T. Two waves share a SIMD, so one's softmax runs
-// beside the other's products.
+// order as the result rows of S^T.
 template <int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   constexpr int kRows = 32 * NW;

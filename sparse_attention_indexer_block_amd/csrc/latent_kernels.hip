@@ -751,11 +751,11 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
         l *= f;
         if (begun) {
 #pragma unroll
-        for (int d = 0; d < 16; ++d) {
-          in_agprs(o[d]);
-          o[d] *= f;
-          in_agprs(o[d]);
-        }
+          for (int d = 0; d < 16; ++d) {
+            in_agprs(o[d]);
+            o[d] *= f;
+            in_agprs(o[d]);
+          }
         }
       }
       bf16x8 pb[2];
@@ -969,10 +969,10 @@ AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
     pl.row_tiles = (int)row_tiles;
     const int most = (int)std::max<int64_t>(1, std::min<int64_t>(256 / row_tiles, tiles));
     for (int want = 1;; want = std::min(2 * want, most)) {
-      pl.tiles_per_split = cdiv(tiles, want);
-      pl.splits = cdiv(tiles, pl.tiles_per_split);
+      const int share = cdiv(tiles, want);  // tiles of a split
+      pl.splits = cdiv(tiles, share);
       const double rounds = (double)((row_tiles * pl.splits + 255) / 256);
-      double cost = rounds * (w.fixed + pl.tiles_per_split * w.tile);
+      double cost = rounds * (w.fixed + share * w.tile);
       if (pl.splits > 1) cost += 4.0 + (double)pl.splits * T * H * (kLatent * 4) / 5.0e6;
       if (best.nq == 0 || cost < least) best = pl, least = cost;
       if (want == most) break;
