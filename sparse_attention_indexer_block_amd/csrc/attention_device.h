@@ -39,13 +39,16 @@ __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
       : "memory");
 }
 // The same from base + off, base uniform over the wave. It may come from a lane
-// read, after which a memory instruction has to wait five states for it.
+// read, after which a memory instruction would have to wait five states for it;
+// a scalar move of it waits by itself.
 __device__ __forceinline__ void copy16_to_lds_at(const void* base, uint32_t off, uint32_t lds) {
+  const void* b;
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 4\n\t"
-      "global_load_lds_dwordx4 %1, %2"
-      :
+      "s_mov_b64 %0, %3\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %0"
+      : "=&s"(b)
       : "s"(lds), "v"(off), "s"(base)
       : "memory");
 }

@@ -166,18 +166,32 @@ __device__ __forceinline__ bf16x8 masked(bf16x8 a, u32x4 m) {
 
 // Copies a tile to LDS, one instruction (1 KB) at a time: a wave that issues them
 // back to back stalls, so they are spread over the products of the tile before.
-// Wave w copies key rows 16 w .. 16 w + 15. aim() takes the tile's cache rows (lane
-// i: key i, or -1, which reads zeros) and leaves little to do per copy.
+// Wave w copies key rows 16 w .. 16 w + 15, eight at a time, in two halves. aim()
+// takes the tile's cache rows (lane i: key i, or -1, which reads zeros) and
+// leaves little to do per copy: the addresses of a half's rows lie in the first
+// lanes of every 16, from where a copy takes its one (a lane read) or two (spread
+// over 32 lanes each by row_newbcast), and flip() brings up the other half's.
 template <class Tile, bool FP8>
 struct TileCopy {
   static constexpr int kPerEight = FP8 ? 5 : 9;  // copies of eight rows: the rows, then their rotary values
   static constexpr int kCopies = 2 * kPerEight;
+  static constexpr int kRowsACopy = FP8 ? 2 : 1;
   const LatentArgs& p;
   int w, lane;
-  uint64_t mine;       // address of key row `lane`
+  int half;            // the half that is up
+  uint32_t off;        // the lane's chunk of a copy, in the order of the half's first row
+  uint64_t held;       // address of key row own_row()
   int rot[2];          // the lane's rotary rows, counted from rot_base
   uint64_t rot_base;
 
+  __device__ __forceinline__ TileCopy(const LatentArgs& a, int w_, int lane_) : p(a), w(w_), lane(lane_), half(0) {
+    off = FP8 ? ((lane & 31) ^ Tile::swz(16 * w + (lane >> 5))) * 16 : (lane ^ Tile::swz(16 * w)) * 16;
+  }
+  // the row of the tile whose address lane i holds
+  __device__ __forceinline__ int own_row() const {
+    const int i = lane & 7;
+    return 16 * w + (lane & 8) + (FP8 ? 2 * (i & 3) + (lane >> 5) : i);
+  }
   __device__ __forceinline__ uint64_t address(const void* from, int row, int stride, int offset) const {
     return row >= 0 ? (uint64_t)(uintptr_t)from + (uint64_t)(uint32_t)row * (uint32_t)stride + offset
                     : (uint64_t)(uintptr_t)g_zero_row;
@@ -187,39 +201,53 @@ struct TileCopy {
   __device__ __forceinline__ void aim_q(const Unit& u0, const Unit& u1) {
     static_assert(!FP8, "queries are bf16 rows");
     constexpr int kStride = 2 * (kLatent + kRotary);
-    mine = (lane & 31) < (lane < 32 ? u0.rows : u1.rows)
-               ? (uint64_t)(uintptr_t)p.q + (uint64_t)((lane < 32 ? u0.row : u1.row) + (lane & 31)) * kStride
-               : (uint64_t)(uintptr_t)g_zero_row;
-    rot_base = (uint64_t)(uintptr_t)p.q + (uint64_t)(w < 2 ? u0.row : u1.row) * kStride;
+    const Unit& u = w < 2 ? u0 : u1;
+    rot_base = (uint64_t)(uintptr_t)p.q + (uint64_t)u.row * kStride;
+    const int own = own_row() & 31;
+    held = own < u.rows ? rot_base + (uint64_t)(uint32_t)own * kStride : (uint64_t)(uintptr_t)g_zero_row;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 16 * (w & 1) + 8 * i + (lane >> 3);
-      rot[i] = r < (w < 2 ? u0.rows : u1.rows) ? r : -1;
+      rot[i] = r < u.rows ? r : -1;
     }
   }
   __device__ __forceinline__ void aim(int rows) {
     rot_base = (uint64_t)(uintptr_t)(FP8 ? (const void*)p.rope : p.c);
-    mine = address(p.c, rows, FP8 ? kLatent : 2 * (kLatent + kRotary), 0);
+    held = address(p.c, __shfl(rows, own_row(), kWave), FP8 ? kLatent : 2 * (kLatent + kRotary), 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) rot[i] = __shfl(rows, 16 * w + 8 * i + (lane >> 3), kWave);
   }
-  __device__ __forceinline__ uint64_t row_address(int i) const {
-    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)mine, i);
-    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(mine >> 32), i);
-    return (uint64_t)hi << 32 | lo;
+  // the other half's rows (twice a tile)
+  __device__ __forceinline__ void flip() {
+    held = (uint64_t)(uint32_t)__builtin_amdgcn_mov_dpp((int)(held >> 32), 0x128, 0xf, 0xf, true) << 32 |  // row_ror:8
+           (uint32_t)__builtin_amdgcn_mov_dpp((int)held, 0x128, 0xf, 0xf, true);
+    off ^= Tile::swz(8) * 16;
+    half ^= 1;
   }
-  // copy j of the wave's rows 8 half .. 8 half + 7
-  __device__ __forceinline__ void copy(uint32_t dst, int half, int j) const {
+  template <int I>
+  __device__ __forceinline__ uint64_t spread_address() const {  // what lane I of every 16 holds
+    return (uint64_t)__builtin_amdgcn_mov_dpp((long)held, 0x150 + I, 0xf, 0xf, true);  // row_newbcast:I
+  }
+  __device__ __forceinline__ uint64_t spread_address(int i) const {
+    switch (i) {  // (i is known when this is compiled)
+      case 0: return spread_address<0>();
+      case 1: return spread_address<1>();
+      case 2: return spread_address<2>();
+      default: return spread_address<3>();
+    }
+  }
+  // copy j of the half that is up
+  __device__ __forceinline__ void copy(uint32_t dst, int j) const {
     const int r0 = 16 * w + 8 * half;
     if (j < kPerEight - 1) {
-      if constexpr (FP8) {  // two rows a copy
-        const uint64_t a0 = row_address(r0 + 2 * j), a1 = row_address(r0 + 2 * j + 1);
-        const int row = r0 + 2 * j + (lane >> 5);
-        const uint64_t src = (lane < 32 ? a0 : a1) + (((lane & 31) ^ Tile::swz(row)) * 16);
-        copy16_to_lds(reinterpret_cast<const void*>(src), dst + (r0 + 2 * j) * Tile::kRow);
+      // (swz() permutes bits, so a row's order is an exclusive-or of its parts')
+      const uint32_t at = off ^ (uint32_t)(Tile::swz(kRowsACopy * j) * 16);
+      const uint32_t to = dst + r0 * Tile::kRow + kRowsACopy * j * Tile::kRow;
+      if constexpr (FP8) {
+        copy16_to_lds(reinterpret_cast<const void*>(spread_address(j) + at), to);
       } else {
-        copy16_to_lds_at(reinterpret_cast<const void*>(row_address(r0 + j)), (lane ^ Tile::swz(r0 + j)) * 16,
-                         dst + (r0 + j) * Tile::kRow);
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)held, j), hi = __builtin_amdgcn_readlane((uint32_t)(held >> 32), j);
+        copy16_to_lds_at(reinterpret_cast<const void*>((uint64_t)hi << 32 | lo), at, to);
       }
     } else {
       const int row = r0 + (lane >> 3), s = half ? rot[1] : rot[0];
@@ -229,9 +257,14 @@ struct TileCopy {
                     dst + Tile::kRope + r0 * Tile::kRopeRow);
     }
   }
-  __device__ __forceinline__ void all(uint32_t dst) const {
+  // copy i of both halves, in order
+  __device__ __forceinline__ void next(uint32_t dst, int i) {
+    copy(dst, i % kPerEight);
+    if (i % kPerEight == kPerEight - 1) flip();
+  }
+  __device__ __forceinline__ void all(uint32_t dst) {
 #pragma unroll
-    for (int j = 0; j < kCopies; ++j) copy(dst, j / kPerEight, j % kPerEight);
+    for (int i = 0; i < kCopies; ++i) next(dst, i);
   }
 };
 
@@ -338,7 +371,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
       using Copy = TileCopy<Tile, FP8>;
 #pragma unroll
       for (int j = i * Copy::kCopies / 32; j < (i + 1) * Copy::kCopies / 32; ++j)
-        copies.copy(next_lds, j / Copy::kPerEight, j % Copy::kPerEight);
+        copies.next(next_lds, j);
     };
 
     // ---- scores of keys 16 w + 4 g + 0..3 (result rows) for rows 16 i + lo (columns)
@@ -489,24 +522,29 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   for (int i = 0; i < QT; ++i) {
     const int r = i * 16 + lo;
     const float tot = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
-    if (lo >= un[i].rows) continue;
     const int64_t R = un[i].row + lo;
+    // (the conditions stand side by side: of nested ones the compiler has left
+    // out the end of the inner, and put a copy of a register under its mask)
+    const bool live = lo < un[i].rows, first = live && w == 0 && g == 0;
     if (p.splits > 1) {
       float* po = p.part + ((int64_t)wk.split * nrows + R) * kLatent + 128 * w + 4 * g;
+      if (live) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(po + 16 * d) = o[d][i];
-      if (w == 0 && g == 0) {
+        for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(po + 16 * d) = o[d][i];
+      }
+      if (first) {
         p.part_ml[((int64_t)wk.split * nrows + R) * 2] = m[i];
         p.part_ml[((int64_t)wk.split * nrows + R) * 2 + 1] = tot;
       }
     } else {
       const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
       uint16_t* po = p.out + R * kLatent + 128 * w + 4 * g;
+      if (live) {
 #pragma unroll
-      for (int d = 0; d < 8; ++d)
-        *reinterpret_cast<bf16x4*>(po + 16 * d) = __builtin_convertvector(o[d][i] * inv, bf16x4);
-      if (p.lse && w == 0 && g == 0)
-        p.lse[R] = tot == 0.f ? -INFINITY : (m[i] + log2_fast(tot)) * 0.6931471805599453f;
+        for (int d = 0; d < 8; ++d)
+          *reinterpret_cast<bf16x4*>(po + 16 * d) = __builtin_convertvector(o[d][i] * inv, bf16x4);
+      }
+      if (p.lse && first) p.lse[R] = tot == 0.f ? -INFINITY : (m[i] + log2_fast(tot)) * 0.6931471805599453f;
     }
   }
 }
@@ -691,8 +729,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       constexpr int kMine = TileCopy<Tile, FP8>::kCopies / NS;
       auto spread = [&](int i) {
         if ((i + 1) * kMine / kReads != i * kMine / kReads) {
-          const int j = i * kMine / kReads;
-          copies.copy(next_lds, G == 2 ? j / TileCopy<Tile, FP8>::kPerEight : n0, j % TileCopy<Tile, FP8>::kPerEight);
+          copies.next(next_lds, i * kMine / kReads);
         }
       };
 #pragma unroll
