@@ -7,13 +7,16 @@
 // (4 significant bits): what a reader gets is the coded value itself. Against
 // max|x| / 448 it costs at most one binade at the bottom of E4M3's range.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention_device.h"
 
 namespace misa {
 
-// D / 8 lanes a row, eight values a lane.
+// D / 8 lanes a row, eight values a lane: one read, the row's maximum over its
+// lanes, one write. Bound by memory from about 16384 latent rows on (29.5 MB in 6.7
+// us, 4.4 TB/s), by the launch below (8 rows 2.2 us).
 template <int D, int DR>
 __global__ __launch_bounds__(256) void k_cache_write(CacheArgs p, const uint16_t* x) {
   constexpr int LPR = D / 8;           // lanes of a row
@@ -66,38 +69,71 @@ __global__ __launch_bounds__(256) void k_cache_copy_in(CacheArgs p, const uint16
       *reinterpret_cast<const u32x4*>(x + i * 8);
 }
 
-// Eight values of a row a thread.
-template <int D, int DR, bool FP8>
+// A wave reads R = NI * 512 / D rows, eight values a lane at a time, and asks for
+// all of them before it uses the first: rows lie anywhere, and the more of them
+// are on their way, the less HBM waits.
+template <int D, int DR, bool FP8, int NI>
 __global__ __launch_bounds__(256) void k_cache_read(CacheArgs p, uint16_t* out) {
-  constexpr int CPR = (D + DR) / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)p.n * CPR) return;
-  const int64_t row = i / CPR;
-  const int ch = (int)(i - row * CPR);
-  const int slot = p.slots[row];
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (slot >= 0 && slot < p.rows) {
-    if (!FP8) {
-      v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.c) + (int64_t)slot * (D + DR) + ch * 8);
-    } else if (ch >= D / 8) {
-      v = *reinterpret_cast<const u32x4*>(p.rope + (int64_t)slot * DR + (ch - D / 8) * 8);
-    } else {
-      const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const unsigned char*>(p.c) + (int64_t)slot * D + ch * 8);
-      const float s = p.scale[slot];
+  constexpr int LPR = D / 8, RPI = kWave / LPR, R = NI * RPI, W = D + DR;
+  constexpr int NR = DR ? (R * (DR / 8) + kWave - 1) / kWave : 0;  // rotary chunks a lane
+  const int lane = threadIdx.x & 63;
+  const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * R;
+  if (row0 >= p.n) return;
+  // the slot of row row0 + lane % R, and whether it names a row
+  const int64_t mine = row0 + lane % R;
+  const int slot = p.slots[min(mine, (int64_t)p.n - 1)];
+  const int held = slot >= 0 && slot < p.rows ? slot : -1;
+  const unsigned char* c = static_cast<const unsigned char*>(p.c);
+  using Chunk = std::conditional_t<FP8, u32x2, u32x4>;
+  Chunk v[NI];
+  float sc[NI];
+  int at[NI];
+  u32x4 rot[NR > 0 ? NR : 1];
+  int rat[NR > 0 ? NR : 1];
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {  // (a row that is not there reads row 0 and is dropped)
+    at[j] = __shfl(held, j * RPI + lane / LPR, kWave);
+    const int64_t r = max(at[j], 0);
+    v[j] = *reinterpret_cast<const Chunk*>(c + r * (FP8 ? D : 2 * W) + (lane % LPR) * sizeof(Chunk));
+    if constexpr (FP8) sc[j] = p.scale[r];
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int i = min(j * kWave + lane, R * (DR / 8) - 1);
+    rat[j] = __shfl(held, i / (DR / 8), kWave);
+    const int64_t r = max(rat[j], 0);
+    rot[j] = FP8 ? *reinterpret_cast<const u32x4*>(p.rope + r * DR + i % (DR / 8) * 8)
+                 : *reinterpret_cast<const u32x4*>(c + r * (2 * W) + 2 * D + i % (DR / 8) * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int64_t row = row0 + j * RPI + lane / LPR;
+    u32x4 o;
+    if constexpr (FP8) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float a, b;
+        float x, y;
         bf16x2 r;
-        fp8x2_to_f32<false>(c[k], a, b);
-        r.x = (__bf16)(a * s), r.y = (__bf16)(b * s);
-        v[2 * k] = __builtin_bit_cast(uint32_t, r);
-        fp8x2_to_f32<true>(c[k], a, b);
-        r.x = (__bf16)(a * s), r.y = (__bf16)(b * s);
-        v[2 * k + 1] = __builtin_bit_cast(uint32_t, r);
+        fp8x2_to_f32<false>(v[j][k], x, y);
+        r.x = (__bf16)(x * sc[j]), r.y = (__bf16)(y * sc[j]);
+        o[2 * k] = __builtin_bit_cast(uint32_t, r);
+        fp8x2_to_f32<true>(v[j][k], x, y);
+        r.x = (__bf16)(x * sc[j]), r.y = (__bf16)(y * sc[j]);
+        o[2 * k + 1] = __builtin_bit_cast(uint32_t, r);
       }
+    } else {
+      o = v[j];
     }
+    if (at[j] < 0) o = u32x4{0u, 0u, 0u, 0u};
+    if (row < p.n) *reinterpret_cast<u32x4*>(out + row * W + (lane % LPR) * 8) = o;
   }
-  *reinterpret_cast<u32x4*>(out + i * 8) = v;
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const int i = j * kWave + lane;
+    const int64_t row = row0 + i / (DR / 8);
+    if (rat[j] < 0) rot[j] = u32x4{0u, 0u, 0u, 0u};
+    if (i < R * (DR / 8) && row < p.n) *reinterpret_cast<u32x4*>(out + row * W + D + i % (DR / 8) * 8) = rot[j];
+  }
 }
 
 static unsigned blocks(int64_t items, int per) { return (unsigned)((items + per - 1) / per); }
@@ -108,11 +144,20 @@ static hipError_t write_shape(const LaunchCtx& cx, const CacheArgs& a, bool fp8,
   return cx.launch("k_cache_copy_in", k_cache_copy_in<D + DR>, dim3(blocks((int64_t)a.n * (D + DR) / 8, 256)),
                    dim3(256), 0, a, x);
 }
+template <int D, int DR, bool FP8, int NI>
+static hipError_t read_as(const LaunchCtx& cx, const CacheArgs& a, uint16_t* out) {
+  return cx.launch("k_cache_read", k_cache_read<D, DR, FP8, NI>, dim3(blocks(a.n, 4 * NI * 512 / D)), dim3(256), 0, a, out);
+}
+// Four times the rows a wave once there are more than 2^22 values, enough for
+// every wave slot. Coded latent rows, cold, one / four: 2048 rows 2.3 / 2.5 us,
+// 8192 4.3 / 4.4, 16384 6.7 / 6.2, 131072 54.6 / 47.4 (4.96 TB/s, what a plain
+// copy reaches; a thread for each eight values took 67.0); keys of 128 values:
+// 32768 rows 4.1 / 4.4, 131072 14.7 / 12.7.
 template <int D, int DR>
 static hipError_t read_shape(const LaunchCtx& cx, const CacheArgs& a, bool fp8, uint16_t* out) {
-  const dim3 grid(blocks((int64_t)a.n * (D + DR) / 8, 256));
-  return fp8 ? cx.launch("k_cache_read", k_cache_read<D, DR, true>, grid, dim3(256), 0, a, out)
-             : cx.launch("k_cache_read", k_cache_read<D, DR, false>, grid, dim3(256), 0, a, out);
+  if ((int64_t)a.n * D > ((int64_t)1 << 22))
+    return fp8 ? read_as<D, DR, true, 4>(cx, a, out) : read_as<D, DR, false, 4>(cx, a, out);
+  return fp8 ? read_as<D, DR, true, 1>(cx, a, out) : read_as<D, DR, false, 1>(cx, a, out);
 }
 
 hipError_t launch_cache_write(const LaunchCtx& cx, const CacheArgs& a, bool fp8, const uint16_t* x) {

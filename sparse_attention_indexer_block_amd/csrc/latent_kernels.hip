@@ -985,8 +985,10 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // less to write where the keys are split), 256 run at a time, and partial sums
 // (2 KB a row and split) are written and joined at 5 TB/s after 4 us of launch.
 // Measured against it, lists of 2048 coded keys, 128 heads (16 / 32 / 64 / 128 rows):
-// 8 queries 32 / 33 / 35 / 38 us, 32 queries 77 / 59 / 51 / 53, 256 queries
-// 577 / 344 / 210 / 174, 1024 queries 2307 / 1371 / 803 / 670.
+// 8 queries 30 / 31 / 35 / 35 us, 32 queries 71 / 56 / 49 / 52, 256 queries
+// 539 / 332 / 206 / 171, 1024 queries 2152 / 1306 / 791 / 629; 4 queries of 32 heads
+// over 100003 bf16 keys 146 / 89 / 69 / 65; 512 causal queries of 16 heads over 4096
+// keys, where a unit of 32 rows is half empty, 240 / 153 / 179 / 178.
 AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
   struct Width {
     int rows, unit;
