@@ -278,7 +278,8 @@ typedef struct misa_cache {
  * rotary columns are copied. A power-of-two scale leaves one rounding per
  * value, and code * scale is exact in bf16. A row with an infinity or NaN among
  * its d columns gets scale NaN and NaN codes. Slots >= 0 must be distinct:
- * a row named twice holds either row's values, possibly mixed. n == 0 is a no-op. */
+ * a row named twice holds either row's values, possibly mixed. n == 0 is a no-op.
+ * Limits (MISA_ERR_UNSUPPORTED past them): 2^30 rows of cache, n <= 2^25. */
 misa_status misa_cache_write(const misa_cache* cache, const void* x, int32_t n, const int32_t* slots, void* stream);
 
 /* Reads row slots[i] of the cache into row i of out [n, d + dr] (bf16 bits):
@@ -306,7 +307,8 @@ misa_status misa_cache_read(const misa_cache* cache, const int32_t* slots, int32
  * has no effect on that query. A query without keys gets out = 0
  * and lse = -inf. Scores, weights' totals and sums are held in fp32; a weight is
  * rounded to bf16 for its product with the values. Results do not depend on
- * what else runs; the same call gives the same bits. */
+ * what else runs; the same call gives the same bits.
+ * Limits (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^30, k <= 2^30. */
 typedef struct misa_latent_problem {
   int32_t T;              /* queries (T == 0 is a no-op) */
   int32_t H;              /* heads per query, >= 1 */
@@ -334,7 +336,9 @@ misa_status misa_latent_attention(const misa_latent_problem* p, void* out, float
  * over the keys b .. b + pos[t] of query t that lie in [0, L), b = base[t] (0 if
  * base is NULL; b < 0 leaves no key): packed sequences have their own base each, pos < 0 marks a
  * padded row. Queries may come in any order; neighbours with overlapping keys
- * run fastest. Otherwise as misa_latent_attention. */
+ * run fastest. Otherwise as misa_latent_attention.
+ * Limits (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^30, H <= 2^20,
+ * L <= 2^30, rope_ld <= 2^24. */
 typedef struct misa_expanded_problem {
   int32_t T;
   int32_t H;

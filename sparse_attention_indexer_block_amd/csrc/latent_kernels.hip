@@ -275,6 +275,12 @@ struct TileCopy {
 // LDS reads). So the tile is read from LDS twice whatever NQ is, the
 // accumulators are spread over the waves, and a row's reference and weights stay
 // in the lanes that hold its column. The copy of the next tile runs meanwhile.
+//
+// It serves calls with few rows, which the chain of dependent steps bounds (list,
+// rows, products, weights, products, partial sums), not a rate: one query of 16
+// heads over 2048 coded keys takes 9 us as 32 workgroups of a tile each, and 4 to
+// join them. A tile more costs 2.25 us with 16 rows and 2.7 with 32, of which the
+// products are 0.3 and 0.5: the rest is the copy's latency and the barriers.
 template <int NQ, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
   using Tile = LatentTile<FP8, false>;
@@ -558,6 +564,20 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // workgroup see different numbers of keys (queries side by side in the prefix
 // form), the few tiles that not all of them see in full are taken once for each
 // number, with the keys beyond it left out, by the waves that it belongs to.
+//
+// Bound by the products and what feeds them. A tile and wave of G = 4 has 136
+// products of 32 cycles (4352) and takes about 9000: 470 for the weights' exponentials of
+// each half, which nothing overlaps (a wave fills its SIMD, and its 512 registers
+// leave no room for a second half in flight), 470 to find the next tile, 500 to wait
+// at its end, and the products themselves run at 0.6 of their rate beside the LDS
+// reads (1 KB a product for each of four waves, all that the LDS gives) and copies.
+// 2048 queries of 128 heads, 2048 bf16 keys each: 1150-1250 us, 0.94-1.0 PFLOP/s,
+// against 1.15 that a library product of 8192^3 reaches here; coded keys 1240 us. A
+// workgroup starts and ends in 20 us (queries and results, 278 KB each, move at the
+// rate of HBM while every workgroup starts), which is what a short list costs.
+// Tried and left out: queries straight to registers (short lists 5% faster, decode
+// batches 4% slower), more LDS reads in flight (spills), weights of half a tile
+// beside the products of the other (spills).
 template <int G, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   using Tile = LatentTile<FP8, true>;
@@ -826,100 +846,114 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
 
   // ---- result: lane holds values 32 d + 8 i + 4 h2 + 0..3 of its row
   float tot = sum_halves(l);
-  if constexpr (G == 2) {  // the two waves of a row group, through LDS
+  if constexpr (G == 2) {
+    // the two waves of a row group, through LDS: each takes the other's sums of its
+    // own half of the values, so that both add and both write
     constexpr int kPass = FP8 ? 4 : 8;  // accumulator tiles (4 KB a wave) at a time
-    static_assert(2 * kPass * 4096 <= 2 * Tile::kBytes, "exchange space");
-    f32x4* ex = reinterpret_cast<f32x4*>(&tile[0][0]) + grp * kPass * 256;
-    float* ml = &ksc[0][0];
-    if (half == 1 && h2 == 0) ml[32 * grp + c] = m, ml[64 + 32 * grp + c] = tot;
-    __syncthreads();
-    const float m1 = ml[32 * grp + c], t1 = ml[64 + 32 * grp + c];
-    const float mm = fmaxf(m, m1), f0 = exp2_fast(m - mm), f1 = exp2_fast(m1 - mm);
+    constexpr int kSums = 4 * kPass * 4096;
+    static_assert(kSums + 1024 <= 2 * Tile::kBytes, "exchange space");
+    f32x4* ex = reinterpret_cast<f32x4*>(&tile[0][0]) + w * kPass * 256 + lane;
+    const f32x4* from = reinterpret_cast<const f32x4*>(&tile[0][0]) + (w ^ 2) * kPass * 256 + lane;
+    float* ml = reinterpret_cast<float*>(&tile[0][0] + kSums);
+    if (h2 == 0) ml[64 * half + 32 * grp + c] = m, ml[128 + 64 * half + 32 * grp + c] = tot;
+    float f_own, f_other;
 #pragma unroll
-    for (int d0 = 0; d0 < 16; d0 += kPass) {
-      if (half == 1) {
+    for (int d0 = 0; d0 < 8; d0 += kPass) {
 #pragma unroll
-        for (int d = 0; d < kPass; ++d)
+      for (int d = 0; d < kPass; ++d)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            ex[(d * 4 + i) * 64 + lane] =
-                f32x4{o[d0 + d][4 * i], o[d0 + d][4 * i + 1], o[d0 + d][4 * i + 2], o[d0 + d][4 * i + 3]};
-      }
+        for (int i = 0; i < 4; ++i) {
+          f32x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = half ? o[d0 + d][4 * i + e] : o[8 + d0 + d][4 * i + e];
+          ex[(d * 4 + i) * 64] = x;
+        }
       __syncthreads();
-      if (half == 0) {
-#pragma unroll
-        for (int d = 0; d < kPass; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 x = ex[(d * 4 + i) * 64 + lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d0 + d][4 * i + e] = o[d0 + d][4 * i + e] * f0 + x[e] * f1;
-          }
+      if (d0 == 0) {
+        const float m0 = ml[32 * grp + c], m1 = ml[64 + 32 * grp + c], mm = fmaxf(m0, m1);
+        const float f0 = exp2_fast(m0 - mm), f1 = exp2_fast(m1 - mm);
+        m = mm;
+        tot = ml[128 + 32 * grp + c] * f0 + ml[192 + 32 * grp + c] * f1;
+        f_own = half ? f1 : f0, f_other = half ? f0 : f1;
       }
+#pragma unroll
+      for (int d = 0; d < kPass; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 x = from[(d * 4 + i) * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float own = half ? o[8 + d0 + d][4 * i + e] : o[d0 + d][4 * i + e];
+            o[d0 + d][4 * i + e] = own * f_own + x[e] * f_other;  // (o[0..7]: the wave's half from here on)
+          }
+        }
       __syncthreads();
     }
-    if (half == 1) return;
-    m = mm;
-    tot = tot * f0 + t1 * f1;
   }
   // through LDS (the wave's own part of the tiles), so that rows leave in whole
-  // lines: 16-byte chunks in an order that depends on the row, kSeg bytes of each row at a time
-  constexpr int kSeg = FP8 ? 512 : 1024, kChunks = kSeg / 16;
-  static_assert(4 * 32 * kSeg <= 2 * Tile::kBytes, "room for every wave's rows");
-  const uint32_t mine = tile_lds + w * 32 * kSeg;
+  // lines: 16-byte chunks in an order that depends on the row, `seg` bytes of each row at a time
+  constexpr int kRoom = FP8 ? 512 : 1024;  // bytes a row
+  static_assert(4 * 32 * kRoom <= 2 * Tile::kBytes, "room for every wave's rows");
+  const uint32_t mine = tile_lds + w * 32 * kRoom;
   const int rows_here = un.rows;
   const int64_t R = un.row;
-  auto put = [&](unsigned char* dst, int64_t stride) {  // what is in LDS to rows `stride` apart
-    constexpr int kRows = 64 / kChunks;                 // rows a store
-#pragma unroll 4
+  auto put = [&](unsigned char* dst, int64_t stride, auto seg) {  // what is in LDS to rows `stride` apart
+    constexpr int kSeg = decltype(seg)::value, kChunks = kSeg / 16, kRows = 64 / kChunks;  // rows a store
+#pragma unroll 8
     for (int i = 0; i < rows_here; i += kRows) {
       const int rr = i + lane / kChunks;
       const u32x4 v = lds_read<u32x4>(mine + rr * kSeg + (((lane % kChunks) ^ (rr & 31)) * 16));
       if (rr < rows_here) *reinterpret_cast<u32x4*>(dst + rr * stride + (lane % kChunks) * 16) = v;
     }
   };
-  if (p.splits > 1) {
-    unsigned char* dst = reinterpret_cast<unsigned char*>(p.part + ((int64_t)wk.split * nrows + R) * kLatent);
-    constexpr int kD = kSeg / 128;  // accumulator tiles a pass (32 values, 128 bytes a row)
+  constexpr int kN = G == 2 ? 8 : 16;  // accumulator tiles of the wave: values 32 (8 half) .. of its rows
+  const int col = G == 2 ? 8 * half : 0;
+  {
+    if (p.splits > 1) {
+      constexpr int kSeg = std::min(kRoom, kN * 128), kD = kSeg / 128;  // accumulator tiles a pass (32 values, 128 bytes a row)
+      unsigned char* dst = reinterpret_cast<unsigned char*>(p.part + ((int64_t)wk.split * nrows + R) * kLatent);
 #pragma unroll
-    for (int d0 = 0; d0 < 16; d0 += kD) {
+      for (int d0 = 0; d0 < kN; d0 += kD) {
 #pragma unroll
-      for (int d = 0; d < kD; ++d)
+        for (int d = 0; d < kD; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(mine + c * kSeg + (((8 * d + 2 * i + h2) ^ c) * 16)) =
-              f32x4{o[d0 + d][4 * i], o[d0 + d][4 * i + 1], o[d0 + d][4 * i + 2], o[d0 + d][4 * i + 3]};
-      put(dst + d0 * 128, kLatent * 4);
+          for (int i = 0; i < 4; ++i)
+            *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(mine + c * kSeg + (((8 * d + 2 * i + h2) ^ c) * 16)) =
+                f32x4{o[d0 + d][4 * i], o[d0 + d][4 * i + 1], o[d0 + d][4 * i + 2], o[d0 + d][4 * i + 3]};
+        put(dst + (col + d0) * 128, kLatent * 4, std::integral_constant<int, kSeg>{});
+      }
+    } else {
+      constexpr int kSeg = std::min(kRoom, kN * 64), kD = kSeg / 64;
+      const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
+      unsigned char* dst = reinterpret_cast<unsigned char*>(p.out + R * kLatent);
+#pragma unroll
+      for (int d0 = 0; d0 < kN; d0 += kD) {
+#pragma unroll
+        for (int d = 0; d < kD; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x16& x = o[d0 + d];
+            const f32x4 v = {x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv};
+            *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(mine + c * kSeg + (((4 * d + i) ^ c) * 16) + h2 * 8) =
+                __builtin_convertvector(v, bf16x4);
+          }
+        put(dst + (col + d0) * 64, kLatent * 2, std::integral_constant<int, kSeg>{});
+      }
     }
-    if (c < rows_here && h2 == 0) {
-      p.part_ml[((int64_t)wk.split * nrows + R + c) * 2] = m;
-      p.part_ml[((int64_t)wk.split * nrows + R + c) * 2 + 1] = tot;
-    }
-  } else {
-    const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
-    unsigned char* dst = reinterpret_cast<unsigned char*>(p.out + R * kLatent);
-    constexpr int kD = kSeg / 64;
-#pragma unroll
-    for (int d0 = 0; d0 < 16; d0 += kD) {
-#pragma unroll
-      for (int d = 0; d < kD; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x16& x = o[d0 + d];
-          const f32x4 v = {x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv};
-          *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(mine + c * kSeg + (((4 * d + i) ^ c) * 16) + h2 * 8) =
-              __builtin_convertvector(v, bf16x4);
-        }
-      put(dst + d0 * 64, kLatent * 2);
-    }
-    if (p.lse && c < rows_here && h2 == 0) p.lse[R + c] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
   }
+  const bool first = half == 0 && h2 == 0 && c < rows_here;
+  if (p.splits > 1 && first) {
+    p.part_ml[((int64_t)wk.split * nrows + R + c) * 2] = m;
+    p.part_ml[((int64_t)wk.split * nrows + R + c) * 2 + 1] = tot;
+  }
+  if (p.splits == 1 && p.lse && first) p.lse[R + c] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
 }
 
 // Joins the splits of a row: each split's sums and total weigh 2^(its reference
 // - the largest). WIDTH / 4 threads hold a row; SG such groups take the splits in
 // turn and are added through LDS in a fixed order, and the rest of the workgroup
-// takes further rows.
+// takes further rows. Bound by memory for many rows (4096 rows of 512 values in 4
+// splits: 34 MB in 7 us), by latency for few (4 us).
 template <int WIDTH, int SG>
 __global__ __launch_bounds__(256) void k_join(const float* part, const float* part_ml, int splits, int64_t rows,
                                               uint16_t* out, float* lse) {
