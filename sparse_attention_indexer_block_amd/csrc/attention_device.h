@@ -8,6 +8,7 @@ namespace misa {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -157,18 +158,9 @@ __device__ __forceinline__ Tp anew(Tp x) {
 // change needs stay in the branch.
 __device__ __forceinline__ void in_agprs(f32x16& d) { asm volatile("" : "+a"(d)); }
 
-// A tile whose keys are not the same for all rows of a wave: a value that is
+// In a tile whose keys are not the same for all rows of a wave a value that is
 // not finite must reach the rows that see its key and no other, but weight 0
-// times infinity or NaN is NaN in a matrix product. Operands without such
-// values (the normal case) are used as they are.
-__device__ __forceinline__ bool any_odd(bf16x8 a) {
-  const u32x4 v = __builtin_bit_cast(u32x4, a);
-  bool odd = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    odd |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
-  return odd;
-}
+// times infinity or NaN is NaN in a matrix product.
 // The values of an operand that are (ODD) or are not infinite or NaN; of the
 // first kind only element `keep`, or none if it is negative.
 template <bool ODD>

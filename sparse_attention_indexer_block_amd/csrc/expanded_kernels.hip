@@ -62,19 +62,38 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   const int head = lid / p.row_tiles % p.H, split = lid / p.row_tiles / p.H;
   if (split >= p.splits) return;
 
-  // ---- key ranges: of the lane's query, of the wave and of the workgroup
-  auto range = [&](int t, int& a, int& b) {
-    a = 0, b = 0;
-    if (t >= p.T) return;
-    const int64_t s0 = p.base ? p.base[t] : 0;
-    const int64_t s1 = min((int64_t)p.L, s0 + (int64_t)p.pos[t] + 1);
-    if (s0 < 0 || s1 <= s0) return;
-    a = (int)s0, b = (int)s1;
-  };
+  // ---- key ranges of the workgroup's queries, 64 a load, and Q: all asked for at
+  // once from rows that are there (a read under a condition would be waited for by itself)
   const int t = rt * kRows + 32 * w + c;
-  int s_lo, s_hi;
-  range(t, s_lo, s_hi);
+  int n_pos[kRows / 64], n_base[kRows / 64];
+#pragma unroll
+  for (int i = 0; i < kRows / 64; ++i) n_pos[i] = p.pos[min(rt * kRows + 64 * i + lane, p.T - 1)];
+#pragma unroll
+  for (int i = 0; i < kRows / 64; ++i) n_base[i] = 0;
+  if (p.base) {
+#pragma unroll
+    for (int i = 0; i < kRows / 64; ++i) n_base[i] = p.base[min(rt * kRows + 64 * i + lane, p.T - 1)];
+  }
+  // Q as the B operand: K step ks, lane (query c, half h2): values 16 ks + 8 h2 .. + 7
+  bf16x8 qf[12];
+  {
+    const uint16_t* qr = p.q + ((int64_t)min(t, p.T - 1) * p.H + head) * (kNope + kRotary) + 8 * h2;
+#pragma unroll
+    for (int ks = 0; ks < 12; ++ks) qf[ks] = *reinterpret_cast<const bf16x8*>(qr + 16 * ks);
+  }
   const uint32_t kBig = 0x7fffffffu;
+  int g_lo = (int)kBig, g_hi = 0, s_lo = 0, s_hi = 0;  // of the workgroup; of the lane's query (0, 0: no key)
+#pragma unroll
+  for (int i = 0; i < kRows / 64; ++i) {
+    const int64_t s0 = n_base[i], s1 = min((int64_t)p.L, s0 + (int64_t)n_pos[i] + 1);
+    const bool any = rt * kRows + 64 * i + lane < p.T && s0 >= 0 && s1 > s0;
+    const int lo_i = any ? (int)s0 : 0, hi_i = any ? (int)s1 : 0;
+    if (any) g_lo = min(g_lo, lo_i), g_hi = max(g_hi, hi_i);
+    const int from = 32 * (w & 1) + c;  // (rows 32 w .. of the workgroup)
+    const int own_lo = __shfl(lo_i, from, kWave), own_hi = __shfl(hi_i, from, kWave);
+    s_lo = w >> 1 == i ? own_lo : s_lo;
+    s_hi = w >> 1 == i ? own_hi : s_hi;
+  }
   const bool some = s_hi > s_lo;
   const int w_lo = (int)wave_min_u32(some ? (uint32_t)s_lo : kBig);    // the wave's first key
   const int w_hi = (int)wave_max_u32((uint32_t)s_hi);                  // and end
@@ -82,13 +101,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
   // result at the end, whatever it gathers
   const int f_lo = (int)wave_max_u32(some ? (uint32_t)s_lo : 0u);
   const int f_hi = w_hi == 0 ? 0 : (int)wave_min_u32(some ? (uint32_t)s_hi : kBig);
-  int g_lo = (int)kBig, g_hi = 0;
-#pragma unroll
-  for (int i = 0; i < kRows / 64; ++i) {
-    int a, b;
-    range(rt * kRows + 64 * i + lane, a, b);
-    if (b > a) g_lo = min(g_lo, a), g_hi = max(g_hi, b);
-  }
   g_lo = (int)wave_min_u32((uint32_t)g_lo);
   g_hi = (int)wave_max_u32((uint32_t)g_hi);
   int tile0 = min(g_lo, g_hi) / kAttnTile, tile1 = (g_hi + kAttnTile - 1) / kAttnTile;
@@ -122,14 +134,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
     for (int j = 0; j < kCopies; ++j) copy(tile_lds, tile0 * kAttnTile, j, lane);
   }
 
-  // Q as the B operand: K step ks, lane (query c, half h2): values 16 ks + 8 h2 .. + 7
   const float sm = scale_magnitude(p.sm_log2);
-  bf16x8 qf[12];
   {
     const uint32_t sign = p.sm_log2 < 0.f ? 0x80008000u : 0u;
-    const uint16_t* qr = p.q + ((int64_t)min(t, p.T - 1) * p.H + head) * (kNope + kRotary) + 8 * h2;
 #pragma unroll
-    for (int ks = 0; ks < 12; ++ks) qf[ks] = flip_sign(*reinterpret_cast<const bf16x8*>(qr + 16 * ks), sign);
+    for (int ks = 0; ks < 12; ++ks) qf[ks] = flip_sign(qf[ks], sign);
   }
   f32x16 o[4];
 #pragma unroll
@@ -189,16 +198,20 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       }
       bool odd = false;  // a value is not finite
       if constexpr (MIXED) {
+        const uint32_t first = (uint32_t)(k0 + 4 * h2 - s_lo), seen = (uint32_t)(s_hi - s_lo);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int key = k0 + 32 * n + 8 * (e >> 2) + 4 * h2 + (e & 3);
-            s[n][e] = key >= s_lo && key < s_hi ? s[n][e] : -INFINITY;
-          }
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) odd |= any_odd(read(kKeyReads + i));
-        odd = __any(odd);
+          for (int e = 0; e < 16; ++e) s[n][e] = first + (32 * n + 8 * (e >> 2) + (e & 3)) < seen ? s[n][e] : -INFINITY;
+        // the largest magnitude among the tile's values, in whatever order they lie
+        u16x2 most = {0, 0};
+#pragma unroll
+        for (int i = 0; i < kAttnTile / 4; ++i) {
+          const u32x4 v = lds_read<u32x4>(tb + (ln >> 4) * kKvRow + (ln & 15) * 16 + 4 * i * kKvRow + ((16 ^ (4 * i & 16)) * 16));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, v[x] & 0x7fff7fffu));
+        }
+        odd = __any(max(most.x, most.y) >= 0x7f80);
       }
       float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll

@@ -560,7 +560,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // weights never leave the lanes that formed them (result rows of S^T = C Q^T are
 // keys; the contraction of O^T = C^T P^T takes the keys in that order). With G =
 // 4 a tile serves 128 rows. With G = 2 the two waves of a row group take
-// alternate halves of each tile and are joined at the end. Where the units of a
+// a half of each tile each and are joined at the end. Where the units of a
 // workgroup see different numbers of keys (queries side by side in the prefix
 // form), the few tiles that not all of them see in full are taken once for each
 // number, with the keys beyond it left out, by the waves that it belongs to.
@@ -1019,16 +1019,16 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // less to write where the keys are split), 256 run at a time, and partial sums
 // (2 KB a row and split) are written and joined at 5 TB/s after 4 us of launch.
 // Measured against it, lists of 2048 coded keys, 128 heads (16 / 32 / 64 / 128 rows):
-// 8 queries 30 / 31 / 35 / 35 us, 32 queries 71 / 56 / 49 / 52, 256 queries
-// 539 / 332 / 206 / 171, 1024 queries 2152 / 1306 / 791 / 629; 4 queries of 32 heads
-// over 100003 bf16 keys 146 / 89 / 69 / 65; 512 causal queries of 16 heads over 4096
-// keys, where a unit of 32 rows is half empty, 240 / 153 / 179 / 178.
+// 8 queries 29 / 31 / 31 / 34 us, 32 queries 71 / 56 / 45 / 51, 256 queries
+// 537 / 334 / 197 / 168, 1024 queries 2155 / 1309 / 771 / 641; 4 queries of 32 heads
+// over 100003 bf16 keys 146 / 88 / 65 / 64; 512 causal queries of 16 heads over 4096
+// keys, where a unit of 32 rows is half empty, 241 / 153 / 177 / 180.
 AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
   struct Width {
     int rows, unit;
     double fixed, tile;
   };
-  static const Width widths[] = {{16, 16, 8.0, 2.25}, {32, 16, 11.0, 2.7}, {64, 32, 15.0, 3.15}, {128, 32, 20.0, 5.2}};
+  static const Width widths[] = {{16, 16, 8.0, 2.25}, {32, 16, 11.0, 2.7}, {64, 32, 12.0, 3.1}, {128, 32, 20.0, 5.2}};
   const int tiles = std::max(1, cdiv(keys, kAttnTile));
   AttnPlan best{};
   double least = 0.0;
