@@ -335,12 +335,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
 }
 
 // Queries per workgroup and splits of the keys, by what they cost on this card, in
-// us: 128 queries take 1.65 a tile with four waves and 256 take 3.1 with eight (1.85 and 2.2
-// alone on its compute unit), a workgroup starts and ends in 9, and partial sums
-// (512 bytes a row and split) are written and joined at 5 TB/s after 4 of launch.
-// The queries are taken to be the last of the keys, which is the most work.
-// Measured (4 / 8 waves): 100 queries over 32768 keys, 16 heads, 60 / 64; 2048 and
-// 8192 causal ones 63 / 77 and 432 / 408.
+// us: a tile takes 1.55 of a compute unit with 128 queries (two such workgroups share
+// it) and 1.4 with 256, and 1.3 and 1.45 in a workgroup whose keys are the longest;
+// partial sums (512 bytes a row and split) are written and joined at 2.6 TB/s after 3
+// of launch. The constants are fitted to 111 measured calls (1 to 8192 queries, 1 to
+// 128 heads, 100 to 32768 keys, packed ones among them); what this rule chooses is 3%
+// off the fastest cut in the mean and 23% at worst. The queries are taken to be the last
+// of the keys, which is the most work. Measured (four / eight waves, splits): 300
+// queries of 16 heads in one piece 14 us / 16, in four 17 / 18; 2048 of 16 heads in one
+// 55 / 67, in two 57 / 52; 8192 of 16 heads 432 / 408; 100 over 32768 keys 65 in 32 /
+// 63 in 16; three packed prompts of 1000, 5 heads, 32 / 33 in four.
 AttnPlan expanded_plan(int T, int H, int L) {
   const double tiles = std::max(1, (L + kAttnTile - 1) / kAttnTile);
   const double mean = std::max(tiles - T / (2.0 * kAttnTile), 0.5 * tiles);
@@ -354,8 +358,8 @@ AttnPlan expanded_plan(int T, int H, int L) {
     const int most = (int)std::max(1.0, std::min((nq == 256 ? 256 : 512) / wgs, tiles));
     for (int s = 1;; s = std::min(2 * s, most)) {
       pl.splits = s;
-      const double all = wgs * mean * (nq == 256 ? 3.1 : 1.65) / 256, longest = tiles / s * (nq == 256 ? 2.2 : 1.85);
-      const double cost = std::max(all, longest) + 9.0 + (s > 1 ? 4.0 + 1.0 * s * T * (double)H * (kValue * 4) / 5.0e6 : 0.0);
+      const double all = wgs * mean * (nq == 256 ? 1.4 : 1.55) / 256, longest = tiles / s * (nq == 256 ? 1.45 : 1.3);
+      const double cost = std::max(all, longest) + (s > 1 ? 3.0 + (double)s * T * H * (kValue * 4) / 2.6e6 : 0.0);
       if (best.nq == 0 || cost < least) best = pl, least = cost;
       if (s == most) break;
     }
