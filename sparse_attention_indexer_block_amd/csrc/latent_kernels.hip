@@ -279,7 +279,7 @@ struct TileCopy {
 // It serves calls with few rows, which the chain of dependent steps bounds (list,
 // rows, products, weights, products, partial sums), not a rate: one query of 16
 // heads over 2048 coded keys takes 9 us as 32 workgroups of a tile each, and 4 to
-// join them. A tile more costs 2.25 us with 16 rows and 2.7 with 32, of which the
+// join them. A tile more costs 1.8 us with 16 rows and 2.2 with 32, of which the
 // products are 0.3 and 0.5: the rest is the copy's latency and the barriers.
 template <int NQ, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
@@ -573,8 +573,10 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // reads (1 KB a product for each of four waves, all that the LDS gives) and copies.
 // 2048 queries of 128 heads, 2048 bf16 keys each: 1150-1250 us, 0.94-1.0 PFLOP/s,
 // against 1.15 that a library product of 8192^3 reaches here; coded keys 1240 us. A
-// workgroup starts and ends in 20 us (queries and results, 278 KB each, move at the
-// rate of HBM while every workgroup starts), which is what a short list costs.
+// workgroup starts and ends in 20 us when all do at once (its queries and results,
+// 278 KB, move at the rate of HBM), which is what a short list costs. With G = 2, 32
+// queries of 128 heads over 2048 coded keys each take 39 us and 7 to join four splits:
+// half of it is the start, the exchange between the waves and 2 KB of sums a row and split.
 // Tried and left out: queries straight to registers (short lists 5% faster, decode
 // batches 4% slower), more LDS reads in flight (spills), weights of half a tile
 // beside the products of the other (spills).
@@ -1017,7 +1019,10 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // they cost on this card, in us. A workgroup starts and ends in `fixed`, a tile
 // of 64 keys takes `tile` (more rows amortise the gather of a tile, fewer leave
 // less to write where the keys are split), 256 run at a time, and partial sums
-// (2 KB a row and split) are written and joined at 5 TB/s after 4 us of launch.
+// (2 KB a row and split) are written and joined at 2.3 TB/s after 3.5 of launch and
+// 0.05 a split. The constants are fitted to 500 measured calls (1 to 1024 queries, 3
+// to 128 heads, lists and prefixes of 100 to 100003 keys, codes and bf16); what this
+// rule chooses is 1% off the fastest cut in the mean and 16% at worst.
 // Measured against it, lists of 2048 coded keys, 128 heads (16 / 32 / 64 / 128 rows):
 // 8 queries 29 / 31 / 31 / 34 us, 32 queries 71 / 56 / 45 / 51, 256 queries
 // 537 / 334 / 197 / 168, 1024 queries 2155 / 1309 / 771 / 641; 4 queries of 32 heads
@@ -1028,7 +1033,7 @@ AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
     int rows, unit;
     double fixed, tile;
   };
-  static const Width widths[] = {{16, 16, 8.0, 2.25}, {32, 16, 11.0, 2.7}, {64, 32, 12.0, 3.1}, {128, 32, 20.0, 5.2}};
+  static const Width widths[] = {{16, 16, 9.0, 1.8}, {32, 16, 11.0, 2.2}, {64, 32, 13.0, 2.25}, {128, 32, 12.0, 3.8}};
   const int tiles = std::max(1, cdiv(keys, kAttnTile));
   AttnPlan best{};
   double least = 0.0;
@@ -1046,7 +1051,7 @@ AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
       pl.splits = cdiv(tiles, share);
       const double rounds = (double)((row_tiles * pl.splits + 255) / 256);
       double cost = rounds * (w.fixed + share * w.tile);
-      if (pl.splits > 1) cost += 4.0 + (double)pl.splits * T * H * (kLatent * 4) / 5.0e6;
+      if (pl.splits > 1) cost += 3.5 + 0.05 * pl.splits + (double)pl.splits * T * H * (kLatent * 4) / 2.3e6;
       if (best.nq == 0 || cost < least) best = pl, least = cost;
       if (want == most) break;
     }

@@ -36,7 +36,7 @@ def _dirty(cache, rows, fp8, bad):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("T,H,k", [(128, 40, 64), (16, 20, 3000), (260, 40, 64), (16, 40, 3000), (260, 100, 64), (64, 100, 3000)])
+@pytest.mark.parametrize("T,H,k", [(128, 40, 64), (16, 20, 3000), (260, 40, 64), (16, 40, 3000), (260, 100, 64), (64, 100, 3000), (100, 100, 8192)])
 def test_lists(T, H, k, fp8):
     rng = np.random.default_rng(T + H + k)
     rows = 2 * k + 40
@@ -58,7 +58,7 @@ def test_lists(T, H, k, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("T,H,rows", [(260, 3, 64), (128, 3, 400), (260, 20, 64), (32, 20, 3000), (32, 40, 3000), (520, 3, 64),
+@pytest.mark.parametrize("T,H,rows", [(260, 3, 64), (128, 3, 400), (260, 20, 64), (32, 20, 3000), (32, 40, 3000), (520, 3, 64), (64, 40, 1000),
                                       (260, 3, 3000), (400, 33, 130)])
 @pytest.mark.parametrize("order", ["causal", "any"])
 def test_prefix(T, H, rows, fp8, order):
