@@ -33,11 +33,11 @@ __device__ __forceinline__ int swz_rot(int row) { return (row >> 2) & 7; }
 // Bound by matrix and vector issue together: the two waves of a SIMD take turns (a
 // product of one does not run beside the exponentials of the other, only beside
 // vector work of its own wave), so a tile costs the sum, 40 products of 32 cycles and
-// about 600 of softmax a wave. 8192 causal queries of 16 heads: 352-390 us, 0.88-0.98
+// about 600 of softmax a wave. 8192 causal queries of 16 heads: 331-390 us, 0.88-1.04
 // PFLOP/s, against 1.15 of a library product of 8192^3 (under this load the clock
 // falls to 2.0 GHz). Few queries over a long context are bound by memory: 100 over
-// 32768 keys of 16 heads read 268 MB in 60 us (4.5 TB/s; a copy reaches 4.9), and
-// join in 6. Tried and left out: waves half a tile apart (402 us against 399), halves
+// 32768 keys of 16 heads read 268 MB in 59 us (4.6 TB/s; a copy reaches 4.9), and
+// join in 5. Tried and left out: waves half a tile apart (402 us against 399), halves
 // of a tile interleaved in a wave (500, registers), four LDS buffers (73 against 60 on
 // the long context).
 template <int NW>
