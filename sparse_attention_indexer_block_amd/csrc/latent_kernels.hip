@@ -952,19 +952,19 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
 }
 
 // Joins the splits of a row: each split's sums and total weigh 2^(its reference
-// - the largest). WIDTH / 4 threads hold a row; SG such groups take the splits in
-// turn and are added through LDS in a fixed order, and the rest of the workgroup
-// takes further rows. Bound by memory for many rows (4096 rows of 512 values in 4
-// splits: 34 MB in 7 us), by latency for few (4 us).
-template <int WIDTH, int SG>
+// - the largest). COLS / 4 threads hold COLS of a row's WIDTH values; SG such groups
+// take the splits in turn and are added through LDS in a fixed order, and the rest of
+// the workgroup takes further rows. Bound by memory where there is much (4096 rows of
+// 512 values in 4 splits: 34 MB in 7 us), by latency where there is little (4 us).
+template <int WIDTH, int COLS, int SG>
 __global__ __launch_bounds__(256) void k_join(const float* part, const float* part_ml, int splits, int64_t rows,
                                               uint16_t* out, float* lse) {
-  constexpr int TPR = WIDTH / 4, ROWS = 256 / TPR / SG;
-  __shared__ __attribute__((aligned(16))) float sums[ROWS][SG][WIDTH];
+  constexpr int TPR = COLS / 4, ROWS = 256 / TPR / SG, PARTS = WIDTH / COLS;
+  __shared__ __attribute__((aligned(16))) float sums[ROWS][SG][COLS];
   __shared__ float tots[ROWS][SG];
   const int c = threadIdx.x % TPR, sg = threadIdx.x / TPR % SG, rr = threadIdx.x / TPR / SG;
-  const int64_t r = min((int64_t)blockIdx.x * ROWS + rr, rows - 1);
-  const bool mine = (int64_t)blockIdx.x * ROWS + rr < rows;
+  const int64_t row = (int64_t)(blockIdx.x / PARTS) * ROWS + rr, r = min(row, rows - 1);
+  const int col = (int)(blockIdx.x % PARTS) * COLS + c * 4;
   float top = kNoMax;
   for (int s = threadIdx.x & 31; s < splits; s += 32) top = fmaxf(top, part_ml[((int64_t)s * rows + r) * 2]);
 #pragma unroll
@@ -976,7 +976,7 @@ __global__ __launch_bounds__(256) void k_join(const float* part, const float* pa
     const float* ml = part_ml + ((int64_t)s * rows + r) * 2;
     const float f = exp2_fast(ml[0] - top);
     tot += f * ml[1];
-    acc += *reinterpret_cast<const f32x4*>(part + ((int64_t)s * rows + r) * WIDTH + c * 4) * f;
+    acc += *reinterpret_cast<const f32x4*>(part + ((int64_t)s * rows + r) * WIDTH + col) * f;
   }
   if constexpr (SG > 1) {
     *reinterpret_cast<f32x4*>(&sums[rr][sg][c * 4]) = acc;
@@ -989,28 +989,29 @@ __global__ __launch_bounds__(256) void k_join(const float* part, const float* pa
       tot += tots[rr][i];
     }
   }
-  if (!mine) return;
+  if (row >= rows) return;
   const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);
-  *reinterpret_cast<bf16x4*>(out + r * WIDTH + c * 4) = __builtin_convertvector(acc * inv, bf16x4);
-  if (lse && c == 0) lse[r] = tot == 0.f ? -INFINITY : (top + log2_fast(tot)) * 0.6931471805599453f;
+  *reinterpret_cast<bf16x4*>(out + r * WIDTH + col) = __builtin_convertvector(acc * inv, bf16x4);
+  if (lse && col == 0) lse[r] = tot == 0.f ? -INFINITY : (top + log2_fast(tot)) * 0.6931471805599453f;
 }
 
-template <int WIDTH, int SG>
+template <int WIDTH, int COLS, int SG>
 static hipError_t join_as(const LaunchCtx& cx, const float* part, const float* part_ml, int splits, int64_t rows,
                           uint16_t* out, float* lse) {
-  constexpr int ROWS = 256 / (WIDTH / 4) / SG;
-  return cx.launch("k_join", k_join<WIDTH, SG>, dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(256), 0, part, part_ml,
-                   splits, rows, out, lse);
+  constexpr int ROWS = 256 / (COLS / 4) / SG;
+  return cx.launch("k_join", k_join<WIDTH, COLS, SG>, dim3((unsigned)((rows + ROWS - 1) / ROWS * (WIDTH / COLS))), dim3(256),
+                   0, part, part_ml, splits, rows, out, lse);
 }
 
-// Several groups a row where a row has many splits or there are few rows to fill the card with.
+// A workgroup for 128 values of a row where a row has many splits or there are few
+// rows to fill the card with, otherwise whole rows.
 hipError_t launch_join(const LaunchCtx& cx, const float* part, const float* part_ml, int splits, int64_t rows,
                        int width, uint16_t* out, float* lse) {
   if (width == kLatent)
-    return splits > 8 || rows < 1024 ? join_as<kLatent, 2>(cx, part, part_ml, splits, rows, out, lse)
-                                     : join_as<kLatent, 1>(cx, part, part_ml, splits, rows, out, lse);
-  return splits > 8 || rows < 1024 ? join_as<kValue, 8>(cx, part, part_ml, splits, rows, out, lse)
-                                   : join_as<kValue, 1>(cx, part, part_ml, splits, rows, out, lse);
+    return splits > 8 || rows < 1024 ? join_as<kLatent, 128, 8>(cx, part, part_ml, splits, rows, out, lse)
+                                     : join_as<kLatent, kLatent, 1>(cx, part, part_ml, splits, rows, out, lse);
+  return splits > 8 || rows < 1024 ? join_as<kValue, kValue, 8>(cx, part, part_ml, splits, rows, out, lse)
+                                   : join_as<kValue, kValue, 1>(cx, part, part_ml, splits, rows, out, lse);
 }
 
 static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
