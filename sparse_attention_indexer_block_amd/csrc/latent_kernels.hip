@@ -128,6 +128,18 @@ struct LatentWork {
     if constexpr (LIST) return p.idx[(int64_t)t * p.k + min(ti * kAttnTile + lane, p.k - 1)];
     return -1;
   }
+  // the list entries of the tile after `next`, which was found after tile ti; v: those of
+  // tile ti + 2. To be called when v's load has landed, and says so to the compiler:
+  // it would wait for copies in flight where v is used otherwise.
+  __device__ __forceinline__ int list_after(int ti, int next, int v) const {
+    if constexpr (!LIST) return -1;
+    asm volatile("" : "+v"(v));
+    if (next != ti + 1) {
+      v = list_entry(next + 1);
+      asm volatile("" : "+v"(v));
+    }
+    return v;
+  }
   // the cache row of key 64 * ti + lane, or -1; v: its list entry
   __device__ __forceinline__ int row_of(int ti, int v) const {
     if constexpr (LIST) {
@@ -566,12 +578,14 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // number, with the keys beyond it left out, by the waves that it belongs to.
 //
 // Bound by the products and what feeds them. A tile and wave of G = 4 has 136
-// products of 32 cycles (4352) and takes about 9000: 470 for the weights' exponentials of
+// products of 32 cycles (4352) and takes about 8700: 470 for the weights' exponentials of
 // each half, which nothing overlaps (a wave fills its SIMD, and its 512 registers
-// leave no room for a second half in flight), 470 to find the next tile, 500 to wait
-// at its end, and the products themselves run at 0.6 of their rate beside the LDS
-// reads (1 KB a product for each of four waves, all that the LDS gives) and copies.
-// 2048 queries of 128 heads, 2048 bf16 keys each: 1150-1250 us, 0.94-1.0 PFLOP/s,
+// leave no room for a second half in flight), 500 at its end, where the copies are
+// waited for while the tile after them is found (found after the barrier instead,
+// from list entries a tile younger, 1190 us against 1145), and the products
+// themselves run at 0.6 of their rate beside the LDS reads (1 KB a product for each
+// of four waves, all that the LDS gives) and copies.
+// 2048 queries of 128 heads, 2048 bf16 keys each: 1100-1190 us, 0.98-1.06 PFLOP/s,
 // against 1.15 that a library product of 8192^3 reaches here; coded keys 1240 us. A
 // workgroup starts and ends in 20 us when all do at once (its queries and results,
 // 278 KB, move at the rate of HBM), which is what a short list costs. With G = 2, 32
@@ -652,6 +666,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   const int v0 = wk.list_entry(wk.cur), v1 = wk.list_entry(wk.cur + 1);
   int cur = next_pass(wk.cur, -1, v0, who_cur, rows_cur);
   int nxt = next_pass(after(cur, who_cur), who_cur, cur == wk.cur ? v1 : wk.list_entry(cur + 1), who_nxt, rows_nxt);
+  int v_nn = wk.list_entry(nxt + 1);
   if (FP8 && w == 0) ksc[0][lane] = rows_cur >= 0 ? key_scale(rows_cur) : 0.f;
 
   // Q as the B operand: K step ks, lane (row c, half h2): values 16 ks + 8 h2 .. + 7; with
@@ -716,7 +731,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   int it = 0;
   while (cur < tile_end) {
     const uint32_t tb = tile_lds + (it & 1) * Tile::kBytes;
-    const int v_nn = wk.list_entry(nxt + 1);
+    int v_two = wk.list_entry(nxt + 2);
     const float sc_nxt = key_scale(rows_nxt);
     copies.lane = anew(lane);
     const uint32_t next_lds = tile_lds + ((it + 1) & 1) * Tile::kBytes;  // (no next tile: zeros, unused)
@@ -835,14 +850,19 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+    int rows_nn, who_nn;  // (found while the copies land)
+    const int nn = next_pass(after(nxt, who_nxt), who_nxt, v_nn, who_nn, rows_nn);
+    copies.aim(rows_nn);
     wait_copies();
+    v_nn = wk.list_after(nxt, nn, v_two);
     if (FP8 && w == 0) ksc[(it + 1) & 1][lane] = rows_nxt >= 0 ? sc_nxt : 0.f;  // (no key: zeros, scaled by none)
     lds_barrier();
     cur = nxt;
     rows_cur = rows_nxt;
     who_cur = who_nxt;
-    nxt = next_pass(after(nxt, who_cur), who_cur, v_nn, who_nxt, rows_nxt);
-    copies.aim(rows_nxt);
+    nxt = nn;
+    rows_nxt = rows_nn;
+    who_nxt = who_nn;
     ++it;
   }
 
