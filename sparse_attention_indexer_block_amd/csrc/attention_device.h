@@ -70,6 +70,10 @@ __device__ __forceinline__ uint32_t lds_addr(Tp* p) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
+// The larger value, NaN if one is (fmaxf would first have every operand quieted by
+// an instruction of its own). A row with a NaN score ends as NaN whatever its reference.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Values of lane l ^ 32 (and l ^ 16) exchanged in registers: with both operands
 // the same, the two results hold the lower and the upper halves (odd and even
 // rows of 16 lanes) for every lane.

@@ -213,9 +213,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
         }
         odd = __any(max(most.x, most.y) >= 0x7f80);
       }
-      float top = fmaxf(s[0][0], s[1][0]);
+      float top = max_or_nan(s[0][0], s[1][0]);
 #pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, fmaxf(s[0][e], s[1][e]));
+      for (int e = 1; e < 16; ++e) top = max_or_nan(max_or_nan(top, s[0][e]), s[1][e]);
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
         const float mm = fmaxf(m, top), f = exp2_fast(m - mm);

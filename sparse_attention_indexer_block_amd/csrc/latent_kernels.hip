@@ -816,7 +816,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       }
       float top = s[0];
 #pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+      for (int e = 1; e < 16; ++e) top = max_or_nan(top, s[e]);
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
         const float mm = fmaxf(m, top), f = exp2_fast(m - mm);
