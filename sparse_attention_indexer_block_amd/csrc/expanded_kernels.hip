@@ -33,7 +33,7 @@ __device__ __forceinline__ int swz_rot(int row) { return (row >> 2) & 7; }
 // Bound by matrix and vector issue together: the two waves of a SIMD take turns (a
 // product of one does not run beside the exponentials of the other, only beside
 // vector work of its own wave), so a tile costs the sum, 40 products of 32 cycles and
-// about 600 of softmax a wave. 8192 causal queries of 16 heads: 331-390 us, 0.88-1.04
+// about 500 of softmax a wave. 8192 causal queries of 16 heads: 330-380 us, 0.90-1.04
 // PFLOP/s, against 1.15 of a library product of 8192^3 (under this load the clock
 // falls to 2.0 GHz). Few queries over a long context are bound by memory: 100 over
 // 32768 keys of 16 heads read 268 MB in 59 us (4.6 TB/s; a copy reaches 4.9), and

@@ -585,7 +585,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // from list entries a tile younger, 1190 us against 1145), and the products
 // themselves run at 0.6 of their rate beside the LDS reads (1 KB a product for each
 // of four waves, all that the LDS gives) and copies.
-// 2048 queries of 128 heads, 2048 bf16 keys each: 1100-1190 us, 0.98-1.06 PFLOP/s,
+// 2048 queries of 128 heads, 2048 bf16 keys each: 1100-1200 us, 0.97-1.06 PFLOP/s,
 // against 1.15 that a library product of 8192^3 reaches here; coded keys 1240 us. A
 // workgroup starts and ends in 20 us when all do at once (its queries and results,
 // 278 KB, move at the rate of HBM), which is what a short list costs. With G = 2, 32
