@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void k_cache_copy_in(CacheArgs p, const uint16
 template <int D, int DR, bool FP8, int NI>
 __global__ __launch_bounds__(256) void k_cache_read(CacheArgs p, uint16_t* out) {
   constexpr int LPR = D / 8, RPI = kWave / LPR, R = NI * RPI, W = D + DR;
-  constexpr int NR = DR ? (R * (DR / 8) + kWave - 1) / kWave : 0;  // rotary chunks a lane
+  constexpr int CPR = DR ? DR / 8 : 1, NR = DR ? (R * CPR + kWave - 1) / kWave : 0;  // rotary chunks of a row and of a lane
   const int lane = threadIdx.x & 63;
   const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * R;
   if (row0 >= p.n) return;
@@ -99,11 +99,11 @@ __global__ __launch_bounds__(256) void k_cache_read(CacheArgs p, uint16_t* out) 
   }
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
-    const int i = min(j * kWave + lane, R * (DR / 8) - 1);
-    rat[j] = __shfl(held, i / (DR / 8), kWave);
+    const int i = min(j * kWave + lane, R * CPR - 1);
+    rat[j] = __shfl(held, i / CPR, kWave);
     const int64_t r = max(rat[j], 0);
-    rot[j] = FP8 ? *reinterpret_cast<const u32x4*>(p.rope + r * DR + i % (DR / 8) * 8)
-                 : *reinterpret_cast<const u32x4*>(c + r * (2 * W) + 2 * D + i % (DR / 8) * 16);
+    rot[j] = FP8 ? *reinterpret_cast<const u32x4*>(p.rope + r * DR + i % CPR * 8)
+                 : *reinterpret_cast<const u32x4*>(c + r * (2 * W) + 2 * D + i % CPR * 16);
   }
 #pragma unroll
   for (int j = 0; j < NI; ++j) {
@@ -130,9 +130,9 @@ __global__ __launch_bounds__(256) void k_cache_read(CacheArgs p, uint16_t* out) 
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
     const int i = j * kWave + lane;
-    const int64_t row = row0 + i / (DR / 8);
+    const int64_t row = row0 + i / CPR;
     if (rat[j] < 0) rot[j] = u32x4{0u, 0u, 0u, 0u};
-    if (i < R * (DR / 8) && row < p.n) *reinterpret_cast<u32x4*>(out + row * W + D + i % (DR / 8) * 8) = rot[j];
+    if (i < R * CPR && row < p.n) *reinterpret_cast<u32x4*>(out + row * W + D + i % CPR * 8) = rot[j];
   }
 }
 
