@@ -422,19 +422,21 @@ def cache_read(slots, C, c_scale=None, rope=None, out=None):
 
 def _attention(call, need, p, q, width, with_lse, ws, out):
     """Output, log-sums and workspace of an attention call, and the call."""
-    T, H, dev, device = p.T, p.H, q.get_device(), q.device
-    if out is None:
-        out = torch.empty((T, H, width), dtype=torch.bfloat16, device=device)
-    lse = torch.empty((T, H), dtype=torch.float32, device=device) if with_lse else None
+    T, H, dev = p.T, p.H, q.get_device()
+    fresh = out is None
+    if fresh:
+        out = q.new_empty((T, H, width))
+    lse = q.new_empty((T, H), dtype=torch.float32) if with_lse else None
     n = need(p)
     if ws is not None:
         _dev(ws, "ws")
         if ws.get_device() != dev:
             raise ValueError(f"ws is on GPU {ws.get_device()}, not on GPU {dev}")
     if ws is None or ws.numel() * ws.element_size() < n:
-        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+        ws = q.new_empty(max(n, 1), dtype=torch.uint8)
     # (n is 0 for a call that the library refuses; the call says why)
-    _on(dev, call, p, _arg(out, "out", _BF16, (T, H, width), dev), lse.data_ptr() if with_lse else None, ws.data_ptr(), n)
+    to = out.data_ptr() if fresh else _arg(out, "out", _BF16, (T, H, width), dev)
+    _on(dev, call, p, to, lse.data_ptr() if with_lse else None, ws.data_ptr(), n)
     return (out, lse) if with_lse else out
 
 
