@@ -425,7 +425,7 @@ def _attention(call, need, p, q, width, with_lse, ws, out):
     T, H, dev = p.T, p.H, q.get_device()
     fresh = out is None
     if fresh:
-        out = q.new_empty((T, H, width))
+        out = q.new_empty((T, H, width), dtype=torch.bfloat16)  # (q may be int16 bits)
     lse = q.new_empty((T, H), dtype=torch.float32) if with_lse else None
     n = need(p)
     if ws is not None:
