@@ -370,7 +370,10 @@ const char* misa_last_error(void);
  * a little launch overhead, so time whole calls with it disabled.
  * misa_profile_read synchronises the recorded events and returns, for kernels
  * whose name contains `name_substr`, the summed duration in milliseconds and
- * the launch count; misa_profile_reset drops all records. */
+ * the launch count; misa_profile_reset drops all records. The names of the
+ * attention's kernels end in the rows of a workgroup (k_latent_16, k_latent_32,
+ * k_latent_wide_64, k_latent_wide_128, k_expanded_128, k_expanded_256), and
+ * k_join runs where the keys were split. */
 misa_status misa_profile_enable(int32_t on);
 misa_status misa_profile_read(const char* name_substr, double* total_ms, int64_t* launches);
 misa_status misa_profile_reset(void);

@@ -381,8 +381,8 @@ hipError_t launch_expanded(const LaunchCtx& cx, ExpandedArgs a, const AttnPlan& 
   }
   const int64_t n = (int64_t)pl.row_tiles * pl.splits * a.H;
   const dim3 grid((unsigned)((n + 7) / 8 * 8));
-  const hipError_t e = pl.nq == 256 ? cx.launch("k_expanded", k_expanded<8>, grid, dim3(512), 0, a)
-                                    : cx.launch("k_expanded", k_expanded<4>, grid, dim3(256), 0, a);
+  const hipError_t e = pl.nq == 256 ? cx.launch("k_expanded_256", k_expanded<8>, grid, dim3(512), 0, a)
+                                    : cx.launch("k_expanded_128", k_expanded<4>, grid, dim3(256), 0, a);
   if (e != hipSuccess || pl.splits <= 1) return e;
   return launch_join(cx, a.part, a.part_ml, pl.splits, rows, kValue, a.out, a.lse);
 }

@@ -1086,16 +1086,19 @@ size_t latent_ws_bytes(const AttnPlan& pl, int T, int H) {
   return 256 + rows * pl.splits * (kLatent + 2) * 4;
 }
 
+// (launches are named by the rows of a workgroup, so that a profile says how a call was cut)
 template <int NQ, bool FP8>
 static hipError_t launch_latent_nq(const LaunchCtx& cx, const LatentArgs& a, dim3 grid) {
-  return a.idx ? cx.launch("k_latent", k_latent<NQ, FP8, true>, grid, dim3(256), 0, a)
-               : cx.launch("k_latent", k_latent<NQ, FP8, false>, grid, dim3(256), 0, a);
+  const char* name = NQ == 16 ? "k_latent_16" : "k_latent_32";
+  return a.idx ? cx.launch(name, k_latent<NQ, FP8, true>, grid, dim3(256), 0, a)
+               : cx.launch(name, k_latent<NQ, FP8, false>, grid, dim3(256), 0, a);
 }
 
 template <int G, bool FP8>
 static hipError_t launch_latent_wide(const LaunchCtx& cx, const LatentArgs& a, dim3 grid) {
-  return a.idx ? cx.launch("k_latent_wide", k_latent_wide<G, FP8, true>, grid, dim3(256), 0, a)
-               : cx.launch("k_latent_wide", k_latent_wide<G, FP8, false>, grid, dim3(256), 0, a);
+  const char* name = G == 2 ? "k_latent_wide_64" : "k_latent_wide_128";
+  return a.idx ? cx.launch(name, k_latent_wide<G, FP8, true>, grid, dim3(256), 0, a)
+               : cx.launch(name, k_latent_wide<G, FP8, false>, grid, dim3(256), 0, a);
 }
 
 template <bool FP8>
