@@ -20,7 +20,9 @@ constexpr float kNoMax = -3.0e38f;
 // of two): weights stay below 2^32, far inside fp32 and bf16, and the
 // accumulated sums are rescaled in hardly any tile but the first (with 2^8 one
 // of 32 rows passed it every few tiles). The reference cancels in the quotient,
-// so results do not change beyond fp32 rounding.
+// so results do not change beyond fp32 rounding. Each row's is raised by its own
+// scores alone: a weight is rounded to bf16 against it, and a row's bits must not
+// depend on the rows beside it.
 constexpr float kSlack = 32.0f;
 
 // Starts a copy of 16 bytes a lane from global memory to LDS at lds + 16 * lane

@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       for (int e = 1; e < 16; ++e) top = max_or_nan(max_or_nan(top, s[0][e]), s[1][e]);
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
-        const float mm = fmaxf(m, top), f = exp2_fast(m - mm);
+        const float mm = top > m + kSlack ? top : m, f = exp2_fast(m - mm);
         m = mm;
         l *= f;
 #pragma unroll

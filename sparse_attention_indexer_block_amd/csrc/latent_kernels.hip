@@ -468,12 +468,15 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
     weigh();
     if (__any(high) && lane == 0) raise[it & 1] = 1;
     lds_barrier();
-    if (__builtin_expect(raise[it & 1], 0)) {  // the same for all waves: move the references up, weigh again
+    // the same for all waves: move up the references of the rows that passed theirs (of
+    // no other: a row's bits are its own) and weigh again
+    if (__builtin_expect(raise[it & 1], 0)) {
       float f[QT];
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
         const int r = i * 16 + lo;
-        const float mm = fmaxf(fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r])), m[i]);
+        const float most = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+        const float mm = most > m[i] + kSlack ? most : m[i];
         f[i] = exp2_fast(m[i] - mm);
         m[i] = mm;
         l[i] *= f[i];
@@ -819,7 +822,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       for (int e = 1; e < 16; ++e) top = max_or_nan(top, s[e]);
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
-        const float mm = fmaxf(m, top), f = exp2_fast(m - mm);
+        const float mm = top > m + kSlack ? top : m, f = exp2_fast(m - mm);
         const bool begun = __any(m > kNoMax);  // (before the first key the sums are zero)
         m = mm;
         l *= f;
