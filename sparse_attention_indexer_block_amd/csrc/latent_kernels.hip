@@ -460,7 +460,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         // rounded to bf16 for the matrix cores; the row's total keeps 32 bits
         if constexpr (FP8) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) e[x] = PART && e[x] == 0.f ? 0.f : e[x] * ksc[x];
+          for (int x = 0; x < 4; ++x)  // (a key that the unit does not see is scaled by 0, whatever its scale is)
+            e[x] *= !PART || (seen[i] >> (16 * w + 4 * g + x)) & 1u ? ksc[x] : 0.f;
         }
         *(__attribute__((address_space(3))) bf16x4*)(uintptr_t)(a_pwr + i * 2048) = __builtin_convertvector(e, bf16x4);
       }
