@@ -13,9 +13,11 @@ typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Softmax reference of a row that has seen no key: finite, so that a masked
-// score (-inf) minus it is -inf and weighs 0, and below every score.
-constexpr float kNoMax = -3.0e38f;
+// Softmax reference of a row that has seen no key: the lowest finite number, so
+// that a masked score (-inf) minus it is -inf and weighs 0, and no finite score is
+// below it. (A reference of this size plus kSlack rounds to itself, so that any
+// score but the lowest one raises it, and that one weighs 1 against it.)
+constexpr float kNoMax = -0x1.fffffep127f;
 // A row's reference is raised when a score passes it by this much (in powers
 // of two): weights stay below 2^32, far inside fp32 and bf16, and the
 // accumulated sums are rescaled in hardly any tile but the first (with 2^8 one

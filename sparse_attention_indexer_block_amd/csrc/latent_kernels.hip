@@ -824,7 +824,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       top = max_halves(top) * sm;
       if (__builtin_expect(__any(top > m + kSlack), 0)) {
         const float mm = top > m + kSlack ? top : m, f = exp2_fast(m - mm);
-        const bool begun = __any(m > kNoMax);  // (before the first key the sums are zero)
+        const bool begun = __any(l != 0.f);  // (before a key weighs anything the sums are zero)
         m = mm;
         l *= f;
         if (begun) {

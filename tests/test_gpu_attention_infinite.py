@@ -1,11 +1,11 @@
-"""Scores of minus infinity and values that are infinite, in keys that a query
+"""Scores of minus infinity and near the lowest number, and values that are infinite, in keys that a query
 sees: what the formula gives (a weight of zero times an infinite value is NaN), on
 every width, whatever tile the key lies in."""
 import numpy as np
 import pytest
 import torch
 
-from attention_cut import LATENT, cut_of
+from attention_cut import EXPANDED, LATENT, cut_of
 from attention_parity import SM, U, bf16, f64, gpu, latent_cache
 from oracle.attention import attend, latent_keys
 
@@ -79,3 +79,84 @@ def test_list_with_an_infinite_scale(T, H, k, cut):
     assert ran == cut
     cache["c_scale"][key] = float("inf")
     _check(call(), clean, q, K, lambda t: latent_keys(rows, None, idx[t]), key, [0])
+
+
+# ------------------------------------------------ scores near the lowest number
+
+LN2 = 0.6931471824645996                                       # times log2(e) in fp32: 1
+
+
+def _far_below(rng, T, H, rows, width, rotary, fp8=False):
+    """Queries and a cache whose every score in powers of two is -1.9375 * 2^127 (-3.297e38), by one rotary value."""
+    q = torch.zeros(T, H, width, dtype=torch.bfloat16)
+    q[:, :, width - rotary + 8] = 2.0 ** 64
+    cache, K = latent_cache(rng, rows, fp8)
+    (cache["rope"] if fp8 else cache["C"])[:, 8 if fp8 else 520] = -1.9375 * 2.0 ** 63
+    return q, cache, K
+
+
+def _own_row(out, lse, want, n):
+    """Every key of the query is the same row: its values, and its score plus log n."""
+    assert torch.equal(out.cpu(), want.expand_as(out).to(torch.bfloat16))
+    z = lse.cpu().double()
+    assert bool((z - (-1.9375 * 2.0 ** 127 * LN2 + np.log(n))).abs().max() <= 2.0 ** -21 * 2.3e38)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,k,cut", LISTS)
+def test_list_of_scores_far_below_zero(T, H, k, cut, fp8):
+    q, cache, K = _far_below(np.random.default_rng(k), T, H, 40, 576, 64)
+    if fp8:                                                    # (scales of 1: the values are exact in bf16)
+        q, cache, K = _far_below(np.random.default_rng(k), T, H, 40, 576, 64, True)
+        cache["c_scale"][:] = 1.0
+    vals = cache["C"][:, :512].float()
+    idx = torch.arange(T)[:, None].expand(T, k) % 40
+    ran, (out, lse) = cut_of(lambda: S.latent_attention(q.cuda(), sm_scale=LN2, idx=_ints(idx), with_lse=True, **gpu(cache)), LATENT)
+    assert ran == cut
+    _own_row(out, lse, vals[torch.arange(T) % 40][:, None], k)
+
+
+@pytest.mark.parametrize("T,H,rows,cut", SHARED)
+def test_prefix_of_scores_far_below_zero(T, H, rows, cut):
+    q, cache, K = _far_below(np.random.default_rng(rows), T, H, rows, 576, 64)
+    cache["C"][:] = cache["C"][:1].clone()
+    pos = np.full(T, rows - 1)
+    pos[::2] = rows - 60
+    ran, (out, lse) = cut_of(lambda: S.latent_attention(q.cuda(), sm_scale=LN2, pos=_ints(pos), with_lse=True, **gpu(cache)), LATENT)
+    assert ran == cut
+    _own_row(out, lse, cache["C"][0, :512], rows)
+
+
+@pytest.mark.parametrize("T,H,L,cut", [(300, 16, 300, (128, False)), (300, 2, 5000, (128, True)),
+                                       (500, 256, 512, (256, False)), (500, 64, 3000, (256, True))])
+def test_expanded_scores_far_below_zero(T, H, L, cut):
+    q, _, _ = _far_below(np.random.default_rng(L), T, H, 1, 192, 64)
+    kv = bf16(np.random.default_rng(L), 1, H, 256)
+    rope = torch.zeros(L, 64, dtype=torch.bfloat16)
+    rope[:, 8] = -1.9375 * 2.0 ** 63
+    call = lambda: S.expanded_attention(q.cuda(), kv.cuda().expand(L, H, 256).contiguous(), rope.cuda(),  # noqa: E731
+                                        _ints(np.arange(L - T, L)), LN2, with_lse=True)
+    ran, (out, lse) = cut_of(call, EXPANDED)
+    assert ran == cut
+    _own_row(out, lse, kv[0, :, 128:], L)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,k,cut", LISTS)
+def test_keys_after_scores_of_the_lowest_number(T, H, k, cut, fp8):
+    # a tile of keys whose scores are the lowest finite number, -(2 - 2^-23) 2^127, in three exact parts; then
+    # keys of score 0, beside which they weigh nothing
+    cache, K = latent_cache(np.random.default_rng(k), 40, fp8)
+    q = torch.zeros(T, H, 576, dtype=torch.bfloat16)
+    q[:, :, 520:523] = 2.0 ** 64
+    rope = cache["rope"] if fp8 else cache["C"][:, 512:]
+    rope[:, 8:11] = 0.0
+    rope[0, 8:11] = -torch.tensor([2 - 2.0 ** -7, 2.0 ** -7 - 2.0 ** -15, 2.0 ** -15 - 2.0 ** -23]).bfloat16() * 2.0 ** 63
+    if fp8:
+        cache["c_scale"][:] = 1.0
+    idx = torch.zeros(T, k, dtype=torch.int64)
+    idx[:, 64:] = 7
+    ran, (out, lse) = cut_of(lambda: S.latent_attention(q.cuda(), sm_scale=LN2, idx=_ints(idx), with_lse=True, **gpu(cache)), LATENT)
+    assert ran == cut
+    assert torch.equal(out.cpu(), cache["C"][7, :512].float().bfloat16().expand(T, H, 512))
+    assert bool((lse.cpu().double() - np.log(k - 64)).abs().max() <= (k + 16) * U + 2.0 ** -20 + 8 * U * np.log(k))
