@@ -305,7 +305,8 @@ misa_status misa_cache_read(const misa_cache* cache, const int32_t* slots, int32
  * Rows outside [0, rows) of the cache are no keys, and base[t] < 0 leaves no
  * key; what a row holds that is not a key of a query (infinities and NaN too)
  * has no effect on that query. A query without keys gets out = 0
- * and lse = -inf. Scores, weights' totals and sums are held in fp32; a weight is
+ * and lse = -inf; one whose keys all score -inf gets out = NaN
+ * (0 / 0) and lse = -inf. Scores, weights' totals and sums are held in fp32; a weight is
  * rounded to bf16 for its product with the values. Results do not depend on
  * what else runs; the same call gives the same bits.
  * Limits (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^30, k <= 2^30. */

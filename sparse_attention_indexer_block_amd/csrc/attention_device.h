@@ -74,6 +74,17 @@ __device__ __forceinline__ uint32_t lds_addr(Tp* p) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
+// What a row's sums are divided by its total with: a row without keys is zeros, and one
+// whose keys all score -inf is 0 / 0 = NaN, here 0 times infinity.
+__device__ __forceinline__ float row_inverse(bool has_keys, float total) { return has_keys ? 1.f / total : 0.f; }
+// log sum exp of a row with reference m (in powers of two): -inf without keys, or if they all score -inf.
+__device__ __forceinline__ float row_log_sum(bool has_keys, float m, float total) {
+  return has_keys ? (m + log2_fast(total)) * 0.6931471805599453f : -INFINITY;
+}
+// The reference that a part of a row without keys is stored with: k_join tells it from a
+// part whose keys all score -inf, and it weighs nothing.
+__device__ __forceinline__ float part_reference(bool has_keys, float m) { return has_keys ? m : -INFINITY; }
+
 // The larger value, NaN if one is (fmaxf would first have every operand quieted by
 // an instruction of its own). A row with a NaN score ends as NaN whatever its reference.
 __device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }

@@ -315,11 +315,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       put(reinterpret_cast<unsigned char*>(p.part + pr * kValue + 32 * d0), (int64_t)p.H * kValue * 4);
     }
     if (c < rows_here && h2 == 0) {
-      p.part_ml[(pr + (int64_t)c * p.H) * 2] = m;
+      p.part_ml[(pr + (int64_t)c * p.H) * 2] = part_reference(some, m);
       p.part_ml[(pr + (int64_t)c * p.H) * 2 + 1] = tot;
     }
   } else {
-    const float inv = tot > 0.f ? 1.f / tot : (tot == 0.f ? 0.f : tot);  // no key: zeros; NaN stays
+    const float inv = row_inverse(some, tot);
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       }
     put(reinterpret_cast<unsigned char*>(p.out + R0 * kValue), (int64_t)p.H * kValue * 2);
     if (p.lse && c < rows_here && h2 == 0)
-      p.lse[R0 + (int64_t)c * p.H] = tot == 0.f ? -INFINITY : (m + log2_fast(tot)) * 0.6931471805599453f;
+      p.lse[R0 + (int64_t)c * p.H] = row_log_sum(some, m, tot);
   }
 }
 

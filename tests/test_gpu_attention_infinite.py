@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from attention_cut import EXPANDED, LATENT, cut_of
-from attention_parity import SM, U, bf16, f64, gpu, latent_cache
+from attention_parity import SM, U, bf16, check_rows, f64, gpu, latent_cache
 from oracle.attention import attend, latent_keys
 
 pytestmark = pytest.mark.gpu
@@ -160,3 +160,97 @@ def test_keys_after_scores_of_the_lowest_number(T, H, k, cut, fp8):
     assert ran == cut
     assert torch.equal(out.cpu(), cache["C"][7, :512].float().bfloat16().expand(T, H, 512))
     assert bool((lse.cpu().double() - np.log(k - 64)).abs().max() <= (k + 16) * U + 2.0 ** -20 + 8 * U * np.log(k))
+
+
+# ---------------------------------------------- queries whose keys all score -inf
+
+def _minus_inf_rows(rng, T, H, rows, fp8, upto):
+    """Rows 0 .. upto - 1 score -inf with every query, by one rotary value; their values are finite."""
+    cache, K = latent_cache(rng, rows, fp8)
+    q = bf16(rng, T, H, 576)
+    q[:, :, 520] = 0.5
+    (cache["rope"] if fp8 else cache["C"])[:upto, 8 if fp8 else 520] = float("-inf")
+    return q, cache, K
+
+
+def _check_minus_inf(got, q, K, keys_of, upto, only):
+    """keys_of(t): the query's keys; those below `upto` score -inf."""
+    out, lse = (x.cpu() for x in got)
+    kinds = set()
+    for t in only:
+        r = keys_of(t)
+        real = r[r >= upto]
+        kind = "none" if not len(r) else "all -inf" if not len(real) else "some"
+        kinds.add(kind)
+        if kind == "none":
+            assert not out[t].any() and bool((lse[t] == -np.inf).all()), t
+        elif kind == "all -inf":
+            assert bool(out[t].isnan().all()) and bool((lse[t] == -np.inf).all()), t
+    check_rows("the other keys", got[0], got[1], q, lambda t, h: (K[keys_of(t)[keys_of(t) >= upto]], K[keys_of(t)[keys_of(t) >= upto]][:, :512]), 512,
+               only=[t for t in only if (keys_of(t) >= upto).any()])
+    assert "all -inf" in kinds
+    return kinds
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,k,cut", LISTS)
+def test_list_of_keys_that_score_minus_infinity(T, H, k, cut, fp8):
+    rng = np.random.default_rng(T + H + k)
+    rows, upto = k + 50, 9
+    q, cache, K = _minus_inf_rows(rng, T, H, rows, fp8, upto)
+    idx = rng.integers(0, rows, (T, k))
+    idx[0] = rng.integers(0, upto, k)                          # all of them -inf
+    if T > 2:
+        idx[1] = -1                                            # no key
+        idx[2] = -1                                            # one, -inf, the rest padding
+        idx[2, k - 2] = 3
+        idx[3, :k - 1] = rng.integers(0, upto, k - 1)          # one that is not, in the last place
+        idx[3, k - 1] = upto
+    call = lambda: S.latent_attention(q.cuda(), sm_scale=SM, idx=_ints(idx), with_lse=True, **gpu(cache))  # noqa: E731
+    ran, got = cut_of(call, LATENT)
+    assert ran == cut
+    _check_minus_inf(got, q, K, lambda t: latent_keys(rows, None, idx[t]), upto, sorted({0, 1, 2, 3, T - 1} & set(range(T))))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("based", [False, True])
+@pytest.mark.parametrize("T,H,rows", [(2, 3, 130), (20, 3, 1000), (260, 3, 130), (128, 3, 400), (260, 20, 130), (130, 20, 700), (520, 3, 130),
+                                      (260, 3, 700), (130, 33, 130), (64, 33, 1000), (130, 70, 130), (70, 70, 2000)])
+def test_prefix_of_keys_that_score_minus_infinity(T, H, rows, based, fp8):
+    rng = np.random.default_rng(T + H + rows)
+    upto = 75                                                  # the first tile and a part of the second
+    q, cache, K = _minus_inf_rows(rng, T, H, rows, fp8, upto)
+    pos = rng.integers(-1, rows, T)
+    pos[0], pos[1], pos[T - 1] = 5, 80, upto - 1
+    if T > 2:
+        pos[2], pos[3], pos[4] = -1, upto, rows - 1
+    base = rng.integers(0, 9, T) if based else np.zeros(T, dtype=np.int64)
+    base[:2] = 0
+    if T == 2:
+        pos[1] = upto - 1
+    args = dict(sm_scale=SM, pos=_ints(pos), base=_ints(base) if based else None, with_lse=True)
+    got = S.latent_attention(q.cuda(), **gpu(cache), **args)
+    _check_minus_inf(got, q, K, lambda t: latent_keys(rows, int(pos[t]), None, int(base[t])), upto,
+                     sorted({0, 1, 2, 3, 4, T - 1} & set(range(T))))
+
+
+@pytest.mark.parametrize("T,H,L,cut", [(300, 16, 300, (128, False)), (300, 2, 5000, (128, True)),
+                                       (500, 256, 512, (256, False)), (500, 64, 3000, (256, True))])
+def test_expanded_keys_that_score_minus_infinity(T, H, L, cut):
+    rng = np.random.default_rng(T + H + L)
+    q, kv, rope = bf16(rng, T, H, 192), bf16(rng, L, H, 256), bf16(rng, L, 64)
+    q[:, :, 136] = 0.5
+    upto = L - 90
+    rope[:upto, 8] = float("-inf")
+    pos = rng.integers(-1, L, T)
+    pos[:6] = [5, upto - 1, -1, upto, L - 1, 0]
+    call = lambda: S.expanded_attention(q.cuda(), kv.cuda(), rope.cuda(), _ints(pos), SM, with_lse=True)  # noqa: E731
+    ran, (out, lse) = cut_of(call, EXPANDED)
+    assert ran == cut
+    n = torch.from_numpy(pos + 1).cuda()
+    assert bool(out[(n > 0) & (n <= upto)].isnan().all()) and not bool(out[n == 0].any())
+    assert bool((lse[n <= upto] == float("-inf")).all()) and bool(lse[n > upto].isfinite().all())
+    kd, rd = f64(kv[:, :2]), f64(rope)
+    check_rows("the other keys", out[:, :2], lse[:, :2], q[:, :2],
+               lambda t, h: (np.concatenate([kd[upto:pos[t] + 1, h, :128], rd[upto:pos[t] + 1]], 1), kd[upto:pos[t] + 1, h, 128:]),
+               128, only=[3, 4])
