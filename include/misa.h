@@ -314,7 +314,7 @@ typedef struct misa_latent_problem {
   int32_t T;              /* queries (T == 0 is a no-op) */
   int32_t H;              /* heads per query, >= 1 */
   int32_t k;              /* entries of a query's list (idx), or 0 */
-  float sm_scale;         /* softmax scale, finite */
+  float sm_scale;         /* softmax scale, at most 2.35e38 in magnitude */
   const void* q;          /* [T,H,576] bf16 bits, 16-byte aligned */
   const int32_t* idx;     /* [T,k] or NULL */
   const int32_t* pos;     /* [T], required iff idx is NULL */

@@ -56,6 +56,8 @@ static misa_status check_sizes(int32_t T, int32_t H, float sm_scale) {
   if (T > (1 << 22)) return fail(MISA_ERR_UNSUPPORTED, "T = %d exceeds 2^22 queries", T);
   if ((int64_t)T * H > kMaxRows) return fail(MISA_ERR_UNSUPPORTED, "T * H = %lld exceeds 2^30", (long long)T * H);
   if (!std::isfinite(sm_scale)) return fail(MISA_ERR_INVALID_ARG, "sm_scale is not finite");
+  if (!std::isfinite(sm_scale * kLog2e))  // (the kernels' exponentials are powers of two)
+    return fail(MISA_ERR_INVALID_ARG, "sm_scale = %g is past 2.35e38 in magnitude", (double)sm_scale);
   return MISA_OK;
 }
 
