@@ -32,8 +32,9 @@ constexpr float kSlack = 32.0f;
 // wait_copies() before the barrier that hands the tile over; written as one
 // instruction here because the compiler would otherwise wait for every copy in
 // flight before any LDS read. No vector register is written, so nothing can be
-// overwritten while it is in flight; M0 is set where it is used, and nothing
-// else in these kernels reads it.
+// overwritten while it is in flight. M0 is set where it is used and nothing else
+// in these files touches it; the compiler reserves it and does not honour a
+// clobber, so a test reads the generated code for that instead.
 __device__ __forceinline__ void copy16_to_lds(const void* src, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
