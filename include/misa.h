@@ -279,6 +279,8 @@ typedef struct misa_cache {
  * value, and code * scale is exact in bf16. A row with an infinity or NaN among
  * its d columns gets scale NaN and NaN codes. Slots >= 0 must be distinct:
  * a row named twice holds either row's values, possibly mixed. n == 0 is a no-op.
+ * One scale serves all d columns: caches with a scale for each part of a row
+ * (128 columns, say) are another format, which nothing here reads or writes.
  * Limits (MISA_ERR_UNSUPPORTED past them): 2^30 rows of cache, n <= 2^25. */
 misa_status misa_cache_write(const misa_cache* cache, const void* x, int32_t n, const int32_t* slots, void* stream);
 
@@ -307,7 +309,10 @@ misa_status misa_cache_read(const misa_cache* cache, const int32_t* slots, int32
  * has no effect on that query. A query without keys gets out = 0
  * and lse = -inf; one whose keys all score -inf gets out = NaN
  * (0 / 0) and lse = -inf. Scores, weights' totals and sums are held in fp32; a weight is
- * rounded to bf16 for its product with the values. Results do not depend on
+ * rounded to bf16 for its product with the values. The values are summed before
+ * they are divided by the total, with weights below 2^32: where the keys of a query
+ * times the largest magnitude of their values (of coded rows: 448 times the scale)
+ * passes 2^96, sums may overflow. Results do not depend on
  * what else runs; the same call gives the same bits.
  * Limits (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^30, k <= 2^30. */
 typedef struct misa_latent_problem {

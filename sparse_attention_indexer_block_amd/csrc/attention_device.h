@@ -19,7 +19,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // score but the lowest one raises it, and that one weighs 1 against it.)
 constexpr float kNoMax = -0x1.fffffep127f;
 // A row's reference is raised when a score passes it by this much (in powers
-// of two): weights stay below 2^32, far inside fp32 and bf16, and the
+// of two): weights stay below 2^32, far inside fp32 and bf16 (and sums over n keys
+// inside fp32 while n times the largest value is below 2^96), and the
 // accumulated sums are rescaled in hardly any tile but the first (with 2^8 one
 // of 32 rows passed it every few tiles). The reference cancels in the quotient,
 // so results do not change beyond fp32 rounding. Each row's is raised by its own

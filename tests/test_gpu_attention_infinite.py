@@ -254,3 +254,31 @@ def test_expanded_keys_that_score_minus_infinity(T, H, L, cut):
     check_rows("the other keys", out[:, :2], lse[:, :2], q[:, :2],
                lambda t, h: (np.concatenate([kd[upto:pos[t] + 1, h, :128], rd[upto:pos[t] + 1]], 1), kd[upto:pos[t] + 1, h, 128:]),
                128, only=[3, 4])
+
+
+# ------------------------------------------------------------- values at their limit
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,k,cut", LISTS)
+def test_values_at_their_limit(T, H, k, cut, fp8):
+    # weights reach 2^31 before a reference is raised: keys times values stay below 2^96
+    rng = np.random.default_rng(T + H + k)
+    rows = 60
+    cache, K = latent_cache(rng, rows, fp8)
+    q = torch.zeros(T, H, 576, dtype=torch.bfloat16)
+    q[:, :, 520] = 1.0
+    large = 2.0 ** (95 - int(np.ceil(np.log2(k))) - 3)         # (the cache's values are below 2^3 without it)
+    rope = cache["rope"] if fp8 else cache["C"][:, 512:]
+    rope[:30, 8], rope[30:, 8] = 0.0, 31.0
+    if fp8:
+        cache["c_scale"] *= large / 448
+        K[:, :512] *= large / 448
+    else:
+        cache["C"][:, :512] = cache["C"][:, :512].clamp(-8, 8) * large
+        K[:, :512] = f64(cache["C"][:, :512])
+    K[:, 512:] = f64(rope)
+    idx = rng.integers(0, 30, (T, k))
+    idx[:, 64:] = rng.integers(30, rows, (T, k - 64))          # (scores rise after the first tile)
+    ran, (out, lse) = cut_of(lambda: S.latent_attention(q.cuda(), sm_scale=LN2, idx=_ints(idx), with_lse=True, **gpu(cache)), LATENT)
+    assert ran == cut
+    check_rows("large values", out, lse, q, lambda t, h: (K[idx[t]], K[idx[t]][:, :512]), 512, sm=LN2, only=[0, T - 1])
