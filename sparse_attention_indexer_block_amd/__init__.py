@@ -25,7 +25,11 @@ Entry points (same names as the C ABI in include/misa.h):
 Inputs of the selection are CUDA (HIP) tensors: q [T,H,128] bfloat16 (or int16 bf16 bits),
 w [T,H] float32, K [L,128] bfloat16 / int16 bits, or uint8 / float8_e4m3fn
 codes with k_scale [L] float32, pos [T] int32. Caches and attention take
-bfloat16 and E4M3FN tensors of the widths that include/misa.h lists.
+bfloat16 and E4M3FN tensors of the widths that include/misa.h lists (bfloat16
+may be given as int16 bits; results are bfloat16).
+
+Every call is for inference: no result carries a gradient, whatever its inputs
+require.
 """
 from __future__ import annotations
 
@@ -460,7 +464,8 @@ def latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None
     """Attention of q [T, H, 576] over latent cache rows (absorbed form): the
     keys idx [T, k] int32 as the selections return them (-1: none), or every
     key up to pos [T] int32; base [T] int32 is the cache row where each query's
-    sequence begins. C, c_scale, rope: see make_cache (d = 512, rotary 64)."""
+    sequence begins. C, c_scale, rope: see make_cache (d = 512, rotary 64). The
+    result carries no gradient (it is detached from q and the cache)."""
     p = make_latent_problem(q, C, sm_scale, pos, idx, c_scale, rope, base)
     return _attention(lib().misa_latent_attention, lib().misa_latent_workspace_bytes, p, q, LATENT, with_lse, ws, out)
 
@@ -484,7 +489,8 @@ def make_expanded_problem(q, kv, rope, pos, sm_scale, base=None) -> ExpandedProb
 def expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False, ws=None, out=None):
     """Attention of q [T, H, 192] over per-head keys and values kv [L, H, 128 +
     128] with rotary keys rope [L, 64] (rows may be strided, as the last columns
-    of read cache rows are): keys base[t] .. base[t] + pos[t] of query t."""
+    of read cache rows are): keys base[t] .. base[t] + pos[t] of query t. The
+    result carries no gradient (it is detached from q, kv and rope)."""
     p = make_expanded_problem(q, kv, rope, pos, sm_scale, base)
     return _attention(lib().misa_expanded_attention, lib().misa_expanded_workspace_bytes, p, q, VALUE, with_lse, ws,
                       out)
