@@ -76,16 +76,17 @@ __device__ __forceinline__ uint32_t lds_addr(Tp* p) {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
 
+// A row's total as it leaves a kernel: -0 says that the row has no keys (the weights of
+// keys add up to +0 or more; +0 if they all score -inf).
+__device__ __forceinline__ float row_total(bool has_keys, float total) { return has_keys ? total : -0.f; }
+__device__ __forceinline__ bool no_keys(float total) { return __float_as_uint(total) == 0x80000000u; }
 // What a row's sums are divided by its total with: a row without keys is zeros, and one
 // whose keys all score -inf is 0 / 0 = NaN, here 0 times infinity.
-__device__ __forceinline__ float row_inverse(bool has_keys, float total) { return has_keys ? 1.f / total : 0.f; }
+__device__ __forceinline__ float row_inverse(float total) { return no_keys(total) ? 0.f : 1.f / total; }
 // log sum exp of a row with reference m (in powers of two): -inf without keys, or if they all score -inf.
-__device__ __forceinline__ float row_log_sum(bool has_keys, float m, float total) {
-  return has_keys ? (m + log2_fast(total)) * 0.6931471805599453f : -INFINITY;
+__device__ __forceinline__ float row_log_sum(float m, float total) {
+  return no_keys(total) ? -INFINITY : (m + log2_fast(total)) * 0.6931471805599453f;
 }
-// The reference that a part of a row without keys is stored with: k_join tells it from a
-// part whose keys all score -inf, and it weighs nothing.
-__device__ __forceinline__ float part_reference(bool has_keys, float m) { return has_keys ? m : -INFINITY; }
 
 // The larger value, NaN if one is (fmaxf would first have every operand quieted by
 // an instruction of its own). A row with a NaN score ends as NaN whatever its reference.

@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
   }
-  const float tot = sum_halves(l);
+  const float tot = row_total(some, sum_halves(l));
   const uint32_t mine = tile_lds + w * 32 * 256;
   const int rows_here = min(32, p.T - (rt * kRows + 32 * w));
   const int64_t R0 = (int64_t)(rt * kRows + 32 * w) * p.H + head;
@@ -315,11 +315,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       put(reinterpret_cast<unsigned char*>(p.part + pr * kValue + 32 * d0), (int64_t)p.H * kValue * 4);
     }
     if (c < rows_here && h2 == 0) {
-      p.part_ml[(pr + (int64_t)c * p.H) * 2] = part_reference(some, m);
+      p.part_ml[(pr + (int64_t)c * p.H) * 2] = m;
       p.part_ml[(pr + (int64_t)c * p.H) * 2 + 1] = tot;
     }
   } else {
-    const float inv = row_inverse(some, tot);
+    const float inv = row_inverse(tot);
 #pragma unroll
     for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
       }
     put(reinterpret_cast<unsigned char*>(p.out + R0 * kValue), (int64_t)p.H * kValue * 2);
     if (p.lse && c < rows_here && h2 == 0)
-      p.lse[R0 + (int64_t)c * p.H] = row_log_sum(some, m, tot);
+      p.lse[R0 + (int64_t)c * p.H] = row_log_sum(m, tot);
   }
 }
 

@@ -543,8 +543,8 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
     const int r = i * 16 + lo;
-    const float tot = (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]);
-    const bool keys = LIST ? it > 0 : un[i].lim > 0;  // (a list's tiles are taken only if they hold one)
+    // (a list's tiles are taken only if they hold a key)
+    const float tot = row_total(LIST ? it > 0 : un[i].lim > 0, (red[0][r] + red[1][r]) + (red[2][r] + red[3][r]));
     const int64_t R = un[i].row + lo;
     // (the conditions stand side by side: of nested ones the compiler has left
     // out the end of the inner, and put a copy of a register under its mask)
@@ -556,18 +556,18 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
         for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(po + 16 * d) = o[d][i];
       }
       if (first) {
-        p.part_ml[((int64_t)wk.split * nrows + R) * 2] = part_reference(keys, m[i]);
+        p.part_ml[((int64_t)wk.split * nrows + R) * 2] = m[i];
         p.part_ml[((int64_t)wk.split * nrows + R) * 2 + 1] = tot;
       }
     } else {
-      const float inv = row_inverse(keys, tot);
+      const float inv = row_inverse(tot);
       uint16_t* po = p.out + R * kLatent + 128 * w + 4 * g;
       if (live) {
 #pragma unroll
         for (int d = 0; d < 8; ++d)
           *reinterpret_cast<bf16x4*>(po + 16 * d) = __builtin_convertvector(o[d][i] * inv, bf16x4);
       }
-      if (p.lse && first) p.lse[R] = row_log_sum(keys, m[i], tot);
+      if (p.lse && first) p.lse[R] = row_log_sum(m[i], tot);
     }
   }
 }
@@ -917,7 +917,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       __syncthreads();
     }
   }
-  const bool keys = LIST ? it > 0 : un.lim > 0;
+  tot = row_total(LIST ? it > 0 : un.lim > 0, tot);
   // through LDS (the wave's own part of the tiles), so that rows leave in whole
   // lines: 16-byte chunks in an order that depends on the row, `seg` bytes of each row at a time
   constexpr int kRoom = FP8 ? 512 : 1024;  // bytes a row
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
       }
     } else {
       constexpr int kSeg = std::min(kRoom, kN * 64), kD = kSeg / 64;
-      const float inv = row_inverse(keys, tot);
+      const float inv = row_inverse(tot);
       unsigned char* dst = reinterpret_cast<unsigned char*>(p.out + R * kLatent);
 #pragma unroll
       for (int d0 = 0; d0 < kN; d0 += kD) {
@@ -971,10 +971,10 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   }
   const bool first = half == 0 && h2 == 0 && c < rows_here;
   if (p.splits > 1 && first) {
-    p.part_ml[((int64_t)wk.split * nrows + R + c) * 2] = part_reference(keys, m);
+    p.part_ml[((int64_t)wk.split * nrows + R + c) * 2] = m;
     p.part_ml[((int64_t)wk.split * nrows + R + c) * 2 + 1] = tot;
   }
-  if (p.splits == 1 && p.lse && first) p.lse[R + c] = row_log_sum(keys, m, tot);
+  if (p.splits == 1 && p.lse && first) p.lse[R + c] = row_log_sum(m, tot);
 }
 
 // Joins the splits of a row: each split's sums and total weigh 2^(its reference
@@ -992,10 +992,13 @@ __global__ __launch_bounds__(256) void k_join(const float* part, const float* pa
   const int64_t row = (int64_t)(blockIdx.x / PARTS) * ROWS + rr, r = min(row, rows - 1);
   const int col = (int)(blockIdx.x % PARTS) * COLS + c * 4;
   float top = -INFINITY;
-  for (int s = threadIdx.x & 31; s < splits; s += 32) top = fmaxf(top, part_ml[((int64_t)s * rows + r) * 2]);
+  for (int s = threadIdx.x & 31; s < splits; s += 32) {
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(part_ml + ((int64_t)s * rows + r) * 2);
+    top = fmaxf(top, no_keys(ml.y) ? -INFINITY : ml.x);
+  }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));  // (32 lanes share a row)
-  const bool keys = top > -INFINITY;  // (part_reference)
+  const bool keys = top > -INFINITY;
   top = fmaxf(top, kNoMax);
   float tot = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -1018,9 +1021,10 @@ __global__ __launch_bounds__(256) void k_join(const float* part, const float* pa
     }
   }
   if (row >= rows) return;
-  const float inv = row_inverse(keys, tot);
+  tot = row_total(keys, tot);
+  const float inv = row_inverse(tot);
   *reinterpret_cast<bf16x4*>(out + r * WIDTH + col) = __builtin_convertvector(acc * inv, bf16x4);
-  if (lse && col == 0) lse[r] = row_log_sum(keys, top, tot);
+  if (lse && col == 0) lse[r] = row_log_sum(top, tot);
 }
 
 template <int WIDTH, int COLS, int SG>
