@@ -15,8 +15,9 @@
 namespace misa {
 
 // D / 8 lanes a row, eight values a lane: one read, the row's maximum over its
-// lanes, one write. Bound by memory from about 16384 latent rows on (29.5 MB in 6.7
-// us, 4.4 TB/s), by the launch below (8 rows 2.2 us).
+// lanes, one write. Bound by memory from about 16384 latent rows on (29.5 MB in 9.1
+// us, 3.2 TB/s, in 6.7 where the rows lie in the caches; 131072 rows 49.5, 4.8 TB/s; keys
+// of 128 values 13.1), by the launch below (8 rows 2.0 us, 5001 keys 2.7).
 template <int D, int DR>
 __global__ __launch_bounds__(256) void k_cache_write(CacheArgs p, const uint16_t* x) {
   constexpr int LPR = D / 8;           // lanes of a row
@@ -55,7 +56,9 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheArgs p, const uint16_t
   if (sub == 0) p.scale[slot] = scale;
 }
 
-// bf16 caches: 16 bytes a thread.
+// bf16 caches: 16 bytes a thread. A copy, bound as one: 131072 latent rows 59 us (5.1
+// TB/s; a plain copy of 1 or 2 GiB reaches 4.9 to 5.1), 16384 10.4, 131072 keys of 128
+// values 15.7, 5001 2.6.
 template <int W>
 __global__ __launch_bounds__(256) void k_cache_copy_in(CacheArgs p, const uint16_t* x) {
   constexpr int CPR = W / 8;
@@ -150,9 +153,10 @@ static hipError_t read_as(const LaunchCtx& cx, const CacheArgs& a, uint16_t* out
 }
 // Four times the rows a wave once there are more than 2^22 values, enough for
 // every wave slot. Coded latent rows, cold, one / four: 2048 rows 2.3 / 2.5 us,
-// 8192 4.3 / 4.4, 16384 6.7 / 6.2, 131072 54.6 / 47.4 (4.96 TB/s, what a plain
-// copy reaches; a thread for each eight values took 67.0); keys of 128 values:
-// 32768 rows 4.1 / 4.4, 131072 14.7 / 12.7.
+// 8192 4.3 / 4.4, 16384 6.7 / 6.2, 131072 54.6 / 47.4 (47 to 50 us, 4.7 to 5.0 TB/s, from
+// run to run, what a plain copy reaches; a thread for each eight values took 67.0); keys
+// of 128 values: 32768 rows 4.1 / 4.4, 131072 14.7 / 12.7. bf16 rows: 131072 latents
+// 63.6 us (4.75 TB/s), 131072 keys 15.3, 2048 latents 3.0.
 template <int D, int DR>
 static hipError_t read_shape(const LaunchCtx& cx, const CacheArgs& a, bool fp8, uint16_t* out) {
   if ((int64_t)a.n * D > ((int64_t)1 << 22))

@@ -33,8 +33,9 @@ __device__ __forceinline__ int swz_rot(int row) { return (row >> 2) & 7; }
 // Bound by matrix and vector issue together: the two waves of a SIMD take turns (a
 // product of one does not run beside the exponentials of the other, only beside
 // vector work of its own wave), so a tile costs the sum, 40 products of 32 cycles and
-// about 500 of softmax a wave. 8192 causal queries of 16 heads: 330-380 us, 0.90-1.04
-// PFLOP/s, against 1.15 of a library product of 8192^3 (under this load the clock
+// about 500 of softmax a wave. 8192 causal queries of 16 heads: 323-350 us, 0.98-1.06
+// PFLOP/s (up to 444 us in the first thirty calls of a process, while the clock
+// recovers from the onset of the load), against 1.15 of a library product of 8192^3 (under this load the clock
 // falls to 2.0 GHz). Few queries over a long context are bound by memory: 100 over
 // 32768 keys of 16 heads read 268 MB in 59 us (4.6 TB/s; a copy reaches 4.9), and
 // join in 5. Tried and left out: waves half a tile apart (402 us against 399), halves
@@ -341,10 +342,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_expanded(ExpandedArgs p) {
 // of launch. The constants are fitted to 111 measured calls (1 to 8192 queries, 1 to
 // 128 heads, 100 to 32768 keys, packed ones among them); what this rule chooses is 3%
 // off the fastest cut in the mean and 23% at worst. The queries are taken to be the last
-// of the keys, which is the most work. Measured (four / eight waves, splits): 300
-// queries of 16 heads in one piece 14 us / 16, in four 17 / 18; 2048 of 16 heads in one
-// 55 / 67, in two 57 / 52; 8192 of 16 heads 432 / 408; 100 over 32768 keys 65 in 32 /
-// 63 in 16; three packed prompts of 1000, 5 heads, 32 / 33 in four.
+// of the keys, which is the most work. Measured, us a call (four / eight waves, splits):
+// 300 queries of 16 heads in one piece 13 / 16, in four 16 / 18; 2048 of 16 heads in one
+// 51 / 64, in two 55 / 50; 8192 of 16 heads 389 / 348; 100 over 32768 keys 70 in 32 /
+// 70 in 16; three packed prompts of 1000, 5 heads, 30 / 30 in four.
 AttnPlan expanded_plan(int T, int H, int L) {
   const double tiles = std::max(1, (L + kAttnTile - 1) / kAttnTile);
   const double mean = std::max(tiles - T / (2.0 * kAttnTile), 0.5 * tiles);

@@ -586,24 +586,31 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // products of 32 cycles (4352) and takes about 8700: 470 for the weights' exponentials of
 // each half, which nothing overlaps (a wave fills its SIMD, and its 512 registers
 // leave no room for a second half in flight), 500 at its end, where the copies are
-// waited for while the tile after them is found (found after the barrier instead,
-// from list entries a tile younger, 1190 us against 1145), and the products
+// waited for and the tile after them is found, one after the other: the search's loop
+// holds a load of list entries, and the compiler waits for all that is in flight at
+// its head (with the search after the barrier, from list entries a tile younger, 1190
+// us against 1145), and the products
 // themselves run at 0.6 of their rate beside the LDS reads (1 KB a product for each
 // of four waves, all that the LDS gives) and copies.
-// 2048 queries of 128 heads, 2048 bf16 keys each: 1100-1200 us, 0.97-1.06 PFLOP/s,
-// against 1.15 that a library product of 8192^3 reaches here; coded keys 1240 us. A
+// 2048 queries of 128 heads, 2048 bf16 keys each: 1085-1145 us, 1.02-1.08 PFLOP/s (up
+// to 1435 in the first ten calls of a process, while the clock recovers from the onset
+// of the load), against 1.15 that a library product of 8192^3 reaches here; coded keys
+// 1200-1225 us. A
 // workgroup starts and ends in 20 us when all do at once (its queries and results,
 // 278 KB, move at the rate of HBM), which is what a short list costs. With G = 2, 32
 // queries of 128 heads over 2048 coded keys each take 39 us and 7 to join four splits:
 // half of it is the start, the exchange between the waves and 2 KB of sums a row and split.
+// Registers: all 512 are taken, and 1 to 7 more with 64 rows and 16 to 19 with 128 are
+// spilled, before and after the tile loop; inside it only the bits that mask a tile which
+// is not full are reloaded (64 rows, prefixes).
 // Tried and left out: queries straight to registers (short lists 5% faster, decode
-// batches 4% slower), more LDS reads in flight (spills), weights of half a tile
-// beside the products of the other (spills).
+// batches 4% slower), more LDS reads in flight and weights of half a tile beside the
+// products of the other (both spill inside the loop).
 template <int G, bool FP8, bool LIST>
 __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
   using Tile = LatentTile<FP8, true>;
   constexpr int NQ = 32 * G, NS = G / 2;  // rows; 32-key steps of a wave per tile
-  constexpr int kAhead = FP8 ? 4 : G == 2 && !LIST ? 5 : 6;  // LDS reads in flight: as many as the registers hold
+  constexpr int kAhead = FP8 ? 4 : G == 2 && !LIST ? 5 : 6;  // LDS reads in flight
   __shared__ __attribute__((aligned(1024))) unsigned char tile[2][Tile::kBytes];
   __shared__ __attribute__((aligned(16))) float ksc[2][kAttnTile];
 
@@ -855,7 +862,7 @@ __global__ __launch_bounds__(256, 1) void k_latent_wide(LatentArgs p) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    int rows_nn, who_nn;  // (found while the copies land)
+    int rows_nn, who_nn;
     const int nn = next_pass(after(nxt, who_nxt), who_nxt, v_nn, who_nn, rows_nn);
     copies.aim(rows_nn);
     wait_copies();
@@ -1056,11 +1063,12 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // 0.05 a split. The constants are fitted to 500 measured calls (1 to 1024 queries, 3
 // to 128 heads, lists and prefixes of 100 to 100003 keys, codes and bf16); what this
 // rule chooses is 1% off the fastest cut in the mean and 16% at worst.
-// Measured against it, lists of 2048 coded keys, 128 heads (16 / 32 / 64 / 128 rows):
-// 8 queries 29 / 31 / 31 / 34 us, 32 queries 71 / 56 / 45 / 51, 256 queries
-// 537 / 334 / 197 / 168, 1024 queries 2155 / 1309 / 771 / 641; 4 queries of 32 heads
-// over 100003 bf16 keys 146 / 88 / 65 / 64; 512 causal queries of 16 heads over 4096
-// keys, where a unit of 32 rows is half empty, 241 / 153 / 177 / 180.
+// Measured, each width with the cheapest of its splits, lists of 2048 coded keys, 128
+// heads (16 / 32 / 64 / 128 rows): 8 queries 30 / 31 / 31 / 39 us, 32 queries
+// 69 / 54 / 43 / 49, 256 queries 535 / 329 / 184 / 163, 1024 queries
+// 2158 / 1318 / 733 / 641; 4 queries of 32 heads over 100003 bf16 keys
+// 153 / 91 / 62 / 61; 512 causal queries of 16 heads over 4096 keys, where a unit of
+// 32 rows is half empty, 247 / 157 / 152 / 157.
 AttnPlan latent_plan(int T, int H, int keys, bool shared_keys) {
   struct Width {
     int rows, unit;
