@@ -598,7 +598,7 @@ __global__ __launch_bounds__(256, 1) void k_latent(LatentArgs p) {
 // 1200-1225 us. A
 // workgroup starts and ends in 20 us when all do at once (its queries and results,
 // 278 KB, move at the rate of HBM), which is what a short list costs. With G = 2, 32
-// queries of 128 heads over 2048 coded keys each take 39 us and 7 to join four splits:
+// queries of 128 heads over 2048 coded keys each take 38 us and 7 to join four splits:
 // half of it is the start, the exchange between the waves and 2 KB of sums a row and split.
 // Registers: all 512 are taken, and 1 to 7 more with 64 rows and 16 to 19 with 128 are
 // spilled, before and after the tile loop; inside it only the bits that mask a tile which
