@@ -46,8 +46,10 @@
  *   - Every array argument is caller-owned, contiguous, row-major DEVICE memory;
  *     the struct misa_problem itself lives in host memory. The library never
  *     allocates or frees device memory: scratch comes from the caller's
- *     workspace `ws` of `ws_bytes` bytes (size it with misa_workspace_bytes;
- *     256-byte alignment is required).
+ *     workspace `ws` of `ws_bytes` bytes (size it with misa_workspace_bytes,
+ *     the attention's with misa_latent_workspace_bytes and
+ *     misa_expanded_workspace_bytes; 256-byte alignment is required). Outputs
+ *     and workspace must not overlap each other or an input.
  *   - `stream` is a hipStream_t (NULL = the legacy default stream). Calls only
  *     enqueue work and return; they never synchronise the host.
  *   - Argument errors are reported synchronously, before anything is enqueued,
@@ -319,7 +321,8 @@ typedef struct misa_latent_problem {
   int32_t T;              /* queries (T == 0 is a no-op) */
   int32_t H;              /* heads per query, >= 1 */
   int32_t k;              /* entries of a query's list (idx), or 0 */
-  float sm_scale;         /* softmax scale, at most 2.35e38 in magnitude */
+  float sm_scale;         /* softmax scale, at most 2.35e38 in magnitude (0 weighs all keys
+                           * alike, but those that score -inf: they weigh 0 as ever) */
   const void* q;          /* [T,H,576] bf16 bits, 16-byte aligned */
   const int32_t* idx;     /* [T,k] or NULL */
   const int32_t* pos;     /* [T], required iff idx is NULL */
