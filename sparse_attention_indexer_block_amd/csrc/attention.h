@@ -1,6 +1,7 @@
 // What the cache and latent-attention kernels share: fixed widths, argument
 // structs and launchers (cache_kernels.hip, latent_kernels.hip,
-// expanded_kernels.hip; argument checks in api_attention.hip).
+// expanded_kernels.hip, tree_kernels.hip, norm_kernels.hip, paged_kernels.hip;
+// argument checks in api_attention.hip and api_paged.hip).
 #pragma once
 
 #include "launch.h"
@@ -75,6 +76,83 @@ struct ExpandedArgs {
 AttnPlan expanded_plan(int T, int H, int L);
 size_t expanded_ws_bytes(const AttnPlan& pl, int T, int H);
 hipError_t launch_expanded(const LaunchCtx& cx, ExpandedArgs a, const AttnPlan& pl, void* ws);
+
+// ---- paged caches (paged_kernels.hip): position j of sequence s lies in row
+// (table[s, j >> page_log2] << page_log2) + (j & (2^page_log2 - 1))
+struct Pages {
+  const int32_t* table;  // [seqs, per]
+  int32_t seqs, per, page_log2;
+};
+struct Rotation {
+  const float* rot;  // [positions, 64]: cosines, then sines
+  int32_t positions;
+  bool pairs;        // values 2i, 2i + 1 turn together, instead of i, i + 32
+};
+struct AppendArgs {
+  CacheArgs cache;       // (slots unused)
+  Pages pages;
+  const uint16_t* x;     // rows of d + dr bf16, x_ld apart
+  int64_t x_ld;
+  const int32_t* seq;    // [n]
+  const int32_t* pos;    // [n] where a row goes
+  const int32_t* turn;   // [n] the position that it is rotated by
+  const void* weight;    // [d] or null: no norm
+  bool weight_f32;
+  double eps;
+  Rotation rot;          // rot null: no rotation
+  int32_t rot_at;        // first rotated column
+};
+hipError_t launch_paged_append(const LaunchCtx& cx, const AppendArgs& a, bool fp8);
+struct RotateArgs {
+  int32_t T, H;
+  const uint16_t* x;     // [T, H, 64], rows x_h and queries x_t elements apart
+  int64_t x_t, x_h;
+  uint16_t* out;
+  int64_t out_t, out_h;
+  const int32_t* pos;    // [T]
+  Rotation rot;
+};
+hipError_t launch_rotate(const LaunchCtx& cx, const RotateArgs& a);
+
+// ---- norm (norm_kernels.hip)
+struct NormArgs {
+  int32_t n, width;
+  const uint16_t* x;         // rows of width bf16, x_ld apart
+  int64_t x_ld;
+  const uint16_t* residual;  // [n, width] or null
+  const void* weight;        // [width]
+  bool weight_f32;
+  double eps;
+  void* y;                   // [n, width] bf16 or codes
+  float* scale;              // [n] or [n, ceil(width / 128)] (codes)
+  uint16_t* sum;             // [n, width] or null
+};
+enum class NormOut { kBf16, kRowCodes, kGroupCodes };
+hipError_t launch_rms_norm(const LaunchCtx& cx, const NormArgs& a, NormOut out);
+
+// ---- attention of drafted tokens (tree_kernels.hip)
+struct TreeArgs : LatentArgs {
+  Pages pages;
+  int32_t N;              // drafted nodes (queries) of a sequence
+  int32_t words;          // 64-bit words of a mask
+  const int32_t* prefix;  // [seqs]
+  const uint64_t* mask;   // [seqs, N, words] or null (chains)
+  // set by the launcher
+  int32_t tiles_a_seq;    // row tiles of a sequence
+  int32_t budget[2];      // splits over all sequences, in either of two cuts
+  int32_t least;          // tiles a split takes at least
+  float fixed, tile;      // what a workgroup and a tile cost (us)
+  int32_t* rec;           // [seqs, 2]: first slot and splits of a sequence
+};
+struct TreePlan {
+  int nq, tiles_a_seq, budget[2], least;
+  float fixed, tile;
+};
+TreePlan tree_plan(int seqs, int N, int H, int words, int longest);
+size_t tree_ws_bytes(const TreePlan& pl, int seqs);
+hipError_t launch_tree(const LaunchCtx& cx, TreeArgs a, const TreePlan& pl, bool fp8, void* ws);
+// The rows of the keys of queries with lists of positions: [T, k + 64 words], -1 where there is none.
+hipError_t launch_tree_lists(const LaunchCtx& cx, const TreeArgs& a, int32_t* lists);
 
 // Joins the partial results of the splits of rows of `width` values.
 hipError_t launch_join(const LaunchCtx& cx, const float* part, const float* part_ml, int splits, int64_t rows,
