@@ -29,6 +29,13 @@
  *                   (absorbed form), on the selected or on all visible keys.
  *   misa_expanded_attention  the same attention over per-head keys and values
  *                   expanded from the latents.
+ *   misa_paged_append  rows of latents or indexer keys into the pages of their
+ *                   sequences, normed, rotated by position and coded on the way.
+ *   misa_rotate     the same rotation of queries.
+ *   misa_tree_attention  latent attention of drafted tokens (a tree of them, a
+ *                   chain, or one) over a paged cache.
+ *   misa_rms_norm   the norm before a layer, with the residual's addition and a
+ *                   result in bf16 or coded.
  *
  * Definitions (the pages give the structure; the exact formulas are fixed here):
  *   z(t,h,s)  = q[t,h,:] . k[s,:]
@@ -47,8 +54,9 @@
  *     the struct misa_problem itself lives in host memory. The library never
  *     allocates or frees device memory: scratch comes from the caller's
  *     workspace `ws` of `ws_bytes` bytes (size it with misa_workspace_bytes,
- *     the attention's with misa_latent_workspace_bytes and
- *     misa_expanded_workspace_bytes; 256-byte alignment is required). Outputs
+ *     the attention's with misa_latent_workspace_bytes,
+ *     misa_expanded_workspace_bytes and misa_tree_workspace_bytes; 256-byte
+ *     alignment is required). Outputs
  *     and workspace must not overlap each other or an input.
  *   - `stream` is a hipStream_t (NULL = the legacy default stream). Calls only
  *     enqueue work and return; they never synchronise the host.
@@ -367,6 +375,157 @@ size_t misa_expanded_workspace_bytes(const misa_expanded_problem* p);
 misa_status misa_expanded_attention(const misa_expanded_problem* p, void* out, float* lse, void* ws, size_t ws_bytes,
                                     void* stream);
 
+/* ------------------------------------------------------------ paged caches
+ *
+ * A misa_cache whose rows belong to pages of `page` rows each; a sequence's
+ * positions lie in the pages that its row of the table names: position j of
+ * sequence s is row table[s, j / page] * page + j % page. A page number below 0 or
+ * whose row lies outside the cache is no page: its positions are not written and are
+ * no keys. A page may belong to several sequences (a shared prompt).
+ * Limits (MISA_ERR_UNSUPPORTED past them): 2^22 sequences, per * page <= 2^28. */
+typedef struct misa_pages {
+  const int32_t* table;   /* [seqs, per] */
+  int32_t seqs;           /* sequences (0 is a no-op) */
+  int32_t per;            /* pages of a sequence, >= 1 */
+  int32_t page;           /* rows of a page, a power of two */
+} misa_pages;
+
+/* The rotation of 64 rotary values by a position: 32 pairs (a, b) become
+ * (a cos - b sin, b cos + a sin) with the cosines and sines of the position's row
+ * of rot; products and sums are formed in fp32. Values i and i + 32 are a pair, or
+ * (pairs = 1) values 2i and 2i + 1; pair i turns by angle i either way. */
+typedef struct misa_rotation {
+  const float* rot;       /* [positions, 64]: 32 cosines, then 32 sines; 16-byte aligned; NULL: no rotation */
+  int32_t positions;      /* >= 1 */
+  int32_t pairs;          /* 0 or 1 */
+} misa_rotation;
+
+typedef enum misa_wdtype {
+  MISA_W_BF16 = 0,
+  MISA_W_F32 = 1
+} misa_wdtype;
+
+/* Appends row i of x to position pos[i] of sequence seq[i], on the way
+ *   1. normed, if weight is given: v = v / sqrt(mean(v^2) + eps) * weight over the
+ *      d coded columns (a latent's rotary values stay out of it),
+ *   2. rotated, if rotation.rot is given, by position turn[i] (pos[i] if turn is
+ *      NULL; a drafted token's place in the cache is not its place in the text):
+ *      columns rot_at .. rot_at + 63, which are the rotary ones of caches that have
+ *      them (rot_at = d) and any aligned 64 of those that do not (dr = 0; rot_at a
+ *      multiple of 64),
+ *   3. coded, if the cache holds codes, as misa_cache_write does, with the scale that
+ *      the values of steps 1 and 2 call for.
+ * Steps 1 and 2 are formed in fp32, and a value is rounded once, as it is stored.
+ * A row whose seq lies outside [0, seqs), whose pos outside [0, per * page), whose
+ * turn outside the rotation's positions (if it is rotated) or whose page is none
+ * writes nothing. Rows must name distinct places: one named twice holds either row's
+ * values, possibly mixed. n == 0 is a no-op. Limit: n <= 2^25. */
+typedef struct misa_append_problem {
+  int32_t n;
+  const void* x;          /* rows of d + dr bf16 bits, x_ld elements apart; 16-byte aligned */
+  int64_t x_ld;           /* >= d + dr, a multiple of 8 */
+  const int32_t* seq;     /* [n] */
+  const int32_t* pos;     /* [n] */
+  const int32_t* turn;    /* [n] or NULL */
+  const void* weight;     /* [d] or NULL; 16-byte aligned */
+  int32_t w_dtype;        /* misa_wdtype */
+  int32_t rot_at;
+  double eps;             /* >= 0 */
+  misa_rotation rotation;
+  misa_pages pages;
+  misa_cache cache;
+} misa_append_problem;
+
+misa_status misa_paged_append(const misa_append_problem* p, void* stream);
+
+/* Rotates the 64 rotary values of H heads of T queries, query t by position pos[t]:
+ * x and out are [T, H, 64] bf16 bits whose queries and heads are x_t and x_h (out_t
+ * and out_h) elements apart (multiples of 8 that are at least 64; 16-byte aligned), so
+ * that both may be columns of wider rows. out may be x itself; otherwise they must not
+ * overlap. A query whose position lies outside the rotation's is not written. */
+typedef struct misa_rotate_problem {
+  int32_t T;
+  int32_t H;
+  const void* x;
+  int64_t x_t, x_h;
+  const int32_t* pos;     /* [T] */
+  misa_rotation rotation;
+} misa_rotate_problem;
+
+misa_status misa_rotate(const misa_rotate_problem* p, void* out, int64_t out_t, int64_t out_h, void* stream);
+
+/* Latent attention (absorbed form, formula and precision as misa_latent_attention) of
+ * N drafted tokens in each of pages.seqs sequences over a paged latent cache. Node i of
+ * sequence s is query s * N + i. Its keys are, with n = prefix[s] committed tokens
+ * (at positions 0 .. n - 1; at most per * page),
+ *   idx NULL:   positions 0 .. n - 1,
+ *   idx given:  positions idx[s,i,j], j < k, with 0 <= idx[s,i,j] < n (a selection of
+ *               the committed tokens; -1 is padding, what occurs twice counts twice),
+ * and the drafted tokens that it sees, at positions n + b for the bits b of its mask
+ * (bit b % 64 of word b / 64), which is to name the node itself and its ancestors; mask
+ * NULL: nodes 0 .. i (a chain; N = 1 is a decode step). The drafted tokens' rows are
+ * appended before. A query whose mask is 0 in every word is padding, and all queries of
+ * a sequence with prefix < 0: they have no key (out = 0, lse = -inf), whatever q holds.
+ * Positions past the table or in no page are no keys. What is not a key of a query has
+ * no effect on it. Sequences may differ in length; the call is planned for a longest
+ * prefix of `longest` (0: per * page), which may be exceeded: it decides how the call
+ * is cut and never what it returns, to within rounding. Results do not depend on what
+ * else runs, and the same call gives the same bits.
+ * Limits (MISA_ERR_UNSUPPORTED past them): N <= 2^16, words <= 1024, seqs * N <= 2^22,
+ * seqs * N * H <= 2^30, k <= 2^24, seqs * N * (k + 64 words) <= 2^31 with idx (words =
+ * ceil(N / 64) where mask is NULL). */
+typedef struct misa_tree_problem {
+  int32_t N;              /* nodes a sequence, >= 1 */
+  int32_t H;              /* heads, >= 1 */
+  int32_t k;              /* entries of a query's list (idx), or 0 */
+  int32_t words;          /* 64-bit words of a mask, or 0 */
+  float sm_scale;         /* as in misa_latent_problem */
+  int32_t longest;        /* >= 0 */
+  const void* q;          /* [seqs,N,H,576] bf16 bits, 16-byte aligned */
+  const int32_t* prefix;  /* [seqs] */
+  const int64_t* mask;    /* [seqs,N,words] or NULL; 8-byte aligned */
+  const int32_t* idx;     /* [seqs,N,k] or NULL */
+  misa_pages pages;
+  misa_cache cache;       /* d = 512, dr = 64 */
+} misa_tree_problem;
+
+/* Bytes of workspace a call needs (0 for an invalid request; at least 256). Pointers'
+ * contents do not matter, but whether idx and mask are NULL does. */
+size_t misa_tree_workspace_bytes(const misa_tree_problem* p);
+
+/* out [seqs,N,H,512] bf16 bits (16-byte aligned); lse [seqs,N,H] float32 or NULL. */
+misa_status misa_tree_attention(const misa_tree_problem* p, void* out, float* lse, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* -------------------------------------------------------------------- norm
+ *
+ * Root-mean-square norm of n rows, with a residual added before it:
+ *   h = x + residual (x without one),  sum = h,  y = h / sqrt(mean(h^2) + eps) * weight
+ * h and y are formed in fp32 (a sum past its range is infinite), the mean square in
+ * fp64, and each result is rounded once. dtype MISA_K_BF16: y is [n, width] bf16 bits.
+ * MISA_K_FP8_E4M3FN: y is [n, width] codes with y = code * scale, scale [n] for the row
+ * (group 0) or [n, ceil(width / 128)] for each 128 columns (group 128), a power of two
+ * chosen as misa_cache_write chooses a row's; what holds an infinity or NaN gets scale
+ * NaN and NaN codes. sum may be residual itself (each value is read before it is
+ * written); no other overlap is allowed.
+ * Limits (MISA_ERR_UNSUPPORTED past them): width <= 16384, n <= 2^25. */
+typedef struct misa_norm_problem {
+  int32_t n;              /* rows (0 is a no-op) */
+  int32_t width;          /* a multiple of 8 */
+  const void* x;          /* rows of width bf16 bits, x_ld elements apart; 16-byte aligned */
+  int64_t x_ld;           /* >= width, a multiple of 8 */
+  const void* residual;   /* [n,width] bf16 bits or NULL; 16-byte aligned */
+  const void* weight;     /* [width], 16-byte aligned */
+  int32_t w_dtype;        /* misa_wdtype */
+  int32_t dtype;          /* misa_kdtype of y */
+  int32_t group;          /* 0 or 128 */
+  double eps;             /* >= 0 */
+} misa_norm_problem;
+
+/* y 16-byte aligned; scale NULL iff y is bf16; sum [n,width] bf16 bits (16-byte aligned)
+ * or NULL (NULL without residual). */
+misa_status misa_rms_norm(const misa_norm_problem* p, void* y, float* scale, void* sum, void* stream);
+
 /* Short static text for a status code. */
 const char* misa_status_str(int32_t status);
 
@@ -381,8 +540,9 @@ const char* misa_last_error(void);
  * whose name contains `name_substr`, the summed duration in milliseconds and
  * the launch count; misa_profile_reset drops all records. The names of the
  * attention's kernels end in the rows of a workgroup (k_latent_16, k_latent_32,
- * k_latent_wide_64, k_latent_wide_128, k_expanded_128, k_expanded_256), and
- * k_join runs where the keys were split. */
+ * k_latent_wide_64, k_latent_wide_128, k_expanded_128, k_expanded_256; k_tree_16,
+ * k_tree_32, k_tree_64, k_tree_128), and k_join or k_tree_join runs where the keys
+ * were split. */
 misa_status misa_profile_enable(int32_t on);
 misa_status misa_profile_read(const char* name_substr, double* total_ms, int64_t* launches);
 misa_status misa_profile_reset(void);

@@ -21,6 +21,13 @@ Entry points (same names as the C ABI in include/misa.h):
                      with_lse=False)                    -> out [T, H, 512] bf16 (, lse [T, H] f32)
     expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False)
                                                         -> out [T, H, 128] bf16 (, lse [T, H] f32)
+    paged_append(x, seq, pos, table, page, C, c_scale=None, rope=None, weight=None, eps=1e-6, rot=None,
+                 turn=None, rot_at=None, pairs=False)   -> None (rows of the pages are written)
+    rotate(x, pos, rot, pairs=False, out=None)          -> out [T, H, 64] bf16
+    tree_attention(q, prefix, table, page, C, sm_scale, c_scale=None, rope=None, mask=None, idx=None,
+                   longest=0, with_lse=False)           -> out [S, N, H, 512] bf16 (, lse [S, N, H] f32)
+    rms_norm(x, weight, eps=1e-6, residual=None, coded=False, group=0)
+                                                        -> y bf16, or codes, scale (, sum with residual)
 
 Inputs of the selection are CUDA (HIP) tensors: q [T,H,128] bfloat16 (or int16 bf16 bits),
 w [T,H] float32, K [L,128] bfloat16 / int16 bits, or uint8 / float8_e4m3fn
@@ -81,6 +88,39 @@ class ExpandedProblem(ctypes.Structure):
                 ("rope_ld", ctypes.c_int64), ("pos", ctypes.c_void_p), ("base", ctypes.c_void_p)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("seqs", ctypes.c_int32), ("per", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_void_p), ("positions", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
+class AppendProblem(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_ld", ctypes.c_int64), ("seq", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("turn", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("w_dtype", ctypes.c_int32), ("rot_at", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("rotation", Rotation), ("pages", Pages), ("cache", Cache)]
+
+
+class RotateProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_t", ctypes.c_int64),
+                ("x_h", ctypes.c_int64), ("pos", ctypes.c_void_p), ("rotation", Rotation)]
+
+
+class TreeProblem(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("k", ctypes.c_int32), ("words", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("longest", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("prefix", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("pages", Pages),
+                ("cache", Cache)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("width", ctypes.c_int32), ("x", ctypes.c_void_p), ("x_ld", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("group", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
 _lib = None
 
 
@@ -112,6 +152,11 @@ def lib() -> ctypes.CDLL:
             "misa_latent_attention": (i32, [ctypes.POINTER(LatentProblem), vp, vp, vp, sz, vp]),
             "misa_expanded_workspace_bytes": (sz, [ctypes.POINTER(ExpandedProblem)]),
             "misa_expanded_attention": (i32, [ctypes.POINTER(ExpandedProblem), vp, vp, vp, sz, vp]),
+            "misa_paged_append": (i32, [ctypes.POINTER(AppendProblem), vp]),
+            "misa_rotate": (i32, [ctypes.POINTER(RotateProblem), vp, ctypes.c_int64, ctypes.c_int64, vp]),
+            "misa_tree_workspace_bytes": (sz, [ctypes.POINTER(TreeProblem)]),
+            "misa_tree_attention": (i32, [ctypes.POINTER(TreeProblem), vp, vp, vp, sz, vp]),
+            "misa_rms_norm": (i32, [ctypes.POINTER(NormProblem), vp, vp, vp, vp]),
             "misa_status_str": (ctypes.c_char_p, [i32]),
             "misa_last_error": (ctypes.c_char_p, []),
             "misa_profile_enable": (i32, [i32]),
@@ -426,11 +471,11 @@ def cache_read(slots, C, c_scale=None, rope=None, out=None):
 
 def _attention(call, need, p, q, width, with_lse, ws, out):
     """Output, log-sums and workspace of an attention call, and the call."""
-    T, H, dev = p.T, p.H, q.get_device()
+    rows, dev = q.shape[:-1], q.get_device()
     fresh = out is None
     if fresh:
-        out = q.new_empty((T, H, width), dtype=torch.bfloat16)  # (q may be int16 bits)
-    lse = q.new_empty((T, H), dtype=torch.float32) if with_lse else None
+        out = q.new_empty((*rows, width), dtype=torch.bfloat16)  # (q may be int16 bits)
+    lse = q.new_empty(rows, dtype=torch.float32) if with_lse else None
     n = need(p)
     if ws is not None:
         _dev(ws, "ws")
@@ -439,7 +484,7 @@ def _attention(call, need, p, q, width, with_lse, ws, out):
     if ws is None or ws.numel() * ws.element_size() < n:
         ws = q.new_empty(max(n, 1), dtype=torch.uint8)
     # (n is 0 for a call that the library refuses; the call says why)
-    to = out.data_ptr() if fresh else _arg(out, "out", _BF16, (T, H, width), dev)
+    to = out.data_ptr() if fresh else _arg(out, "out", _BF16, (*rows, width), dev)
     _on(dev, call, p, to, lse.data_ptr() if with_lse else None, ws.data_ptr(), n)
     return (out, lse) if with_lse else out
 
@@ -494,6 +539,166 @@ def expanded_attention(q, kv, rope, pos, sm_scale, base=None, with_lse=False, ws
     p = make_expanded_problem(q, kv, rope, pos, sm_scale, base)
     return _attention(lib().misa_expanded_attention, lib().misa_expanded_workspace_bytes, p, q, VALUE, with_lse, ws,
                       out)
+
+
+# ---------------------------------------------------------------- paged caches, drafted tokens, norm
+
+_I64, _WEIGHT = (torch.int64,), (torch.bfloat16, torch.int16, torch.float32)
+
+
+def _pages(table, page, dev) -> Pages:
+    (seqs, per), _ = _first(table, "table", _I32, 2)
+    return Pages(_arg(table, "table", _I32, (seqs, per), dev), seqs, per, page)
+
+
+def _weight(weight, width, dev):
+    at = _arg(weight, "weight", _WEIGHT, (width,), dev)
+    return at, 1 if weight.dtype == torch.float32 else 0
+
+
+def _rotation(rot, pairs, dev) -> Rotation:
+    (positions, _), _ = _first(rot, "rot", _F32, 2)
+    return Rotation(_arg(rot, "rot", _F32, (positions, ROTARY), dev), positions, 1 if pairs else 0)
+
+
+def _rows(x, name: str, width: int, dev: int):
+    """Address, count and distance of rows x [n, width] bfloat16 that may be columns of wider ones."""
+    if x is None or not x.is_cuda or x.dtype not in _BF16 or x.get_device() != dev or x.dim() != 2 or x.shape[1] != width:
+        _refuse(x, name, _BF16, ("n", width), dev)
+    ld, inner = x.stride()
+    if x.shape[0] <= 1:
+        ld = width
+    if (inner != 1 and width > 1) or ld < width:
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return x.data_ptr(), x.shape[0], ld
+
+
+def paged_append(x, seq, pos, table, page, C, c_scale=None, rope=None, weight=None, eps=1e-6, rot=None, turn=None,
+                 rot_at=None, pairs=False):
+    """Write row i of x [n, d (+ 64)] bfloat16 (rows may be strided) to position
+    pos[i] of sequence seq[i] (int32 [n]) of a paged cache: position j of
+    sequence s is row table[s, j // page] * page + j % page of C (table int32
+    [seqs, per], page a power of two). On the way the d values are RMS-normed
+    with weight [d] (bfloat16 or float32) and eps, if it is given, and 64 values
+    are rotated by position turn[i] (int32 [n]; pos if None) with rot [positions,
+    64] float32 (cosines, then sines), if it is given: the rotary ones, or columns
+    rot_at .. rot_at + 63 (0) of rows without. pairs: neighbours turn together,
+    instead of values 32 apart. Rows that name no place (pos or seq of -1, say)
+    write nothing; the others must name distinct ones."""
+    c = make_cache(C, c_scale, rope)
+    dev = C.get_device()
+    at, n, ld = _rows(x, "x", c.d + c.dr, dev)
+    p = AppendProblem(n, at, ld, _arg(seq, "seq", _I32, (n,), dev), _arg(pos, "pos", _I32, (n,), dev),
+                      None if turn is None else _arg(turn, "turn", _I32, (n,), dev))
+    if weight is not None:
+        p.weight, p.w_dtype = _weight(weight, c.d, dev)
+        p.eps = eps
+    if rot is not None:
+        p.rotation = _rotation(rot, pairs, dev)
+        p.rot_at = rot_at if rot_at is not None else c.d if c.dr else 0
+    elif rot_at is not None or pairs:
+        raise ValueError("rot_at and pairs are only for a rotation (rot)")
+    p.pages = _pages(table, page, dev)
+    p.cache = c
+    _on(dev, lib().misa_paged_append, p)
+
+
+def _heads(x, name: str, T, H, dev: int):
+    """Address and distances of x [T, H, 64] bfloat16 that may be columns of wider rows."""
+    if x is None or not x.is_cuda or x.dtype not in _BF16 or x.get_device() != dev or tuple(x.shape) != (T, H, ROTARY):
+        _refuse(x, name, _BF16, (T, H, ROTARY), dev)
+    st, sh, inner = x.stride()
+    sh = ROTARY if H == 1 else sh
+    st = H * sh if T <= 1 else st
+    if inner != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return x.data_ptr(), st, sh
+
+
+def rotate(x, pos, rot, pairs=False, out=None):
+    """The 64 rotary values of queries x [T, H, 64] bfloat16 rotated by their
+    positions pos [T] int32, with rot [positions, 64] float32 (cosines, then
+    sines) as paged_append rotates keys. x and out may be columns of wider rows
+    (the last ones of attention queries, say), and out may be x. A query whose
+    position is not one of rot's is not written (without out it is zeros)."""
+    (T, H, _), dev = _first(x, "x", _BF16, 3)
+    at, st, sh = _heads(x, "x", T, H, dev)
+    if out is None:
+        out = x.new_zeros((T, H, ROTARY), dtype=torch.bfloat16)
+    to, ot, oh = _heads(out, "out", T, H, dev)
+    p = RotateProblem(T, H, at, st, sh, _arg(pos, "pos", _I32, (T,), dev), _rotation(rot, pairs, dev))
+    _on(dev, lib().misa_rotate, p, to, ot, oh)
+    return out
+
+
+def make_tree_problem(q, prefix, table, page, C, sm_scale, c_scale=None, rope=None, mask=None, idx=None, longest=0) -> TreeProblem:
+    c = make_cache(C, c_scale, rope)
+    (S, N, H, _), dev = _first(q, "q", _BF16, 4)
+    p = TreeProblem(N, H, 0, 0, sm_scale, longest, _arg(q, "q", _BF16, (S, N, H, LATENT + ROTARY), C.get_device()),
+                    _arg(prefix, "prefix", _I32, (S,), dev), None, None, _pages(table, page, dev), c)
+    if p.pages.seqs != S:
+        raise ValueError(f"table has {p.pages.seqs} sequences, not {S}")
+    if mask is not None:
+        if mask.dim() == 2:
+            p.mask, p.words = _arg(mask, "mask", _I64, (S, N), dev), 1
+        else:
+            (_, _, p.words), _ = _first(mask, "mask", _I64, 3)
+            p.mask = _arg(mask, "mask", _I64, (S, N, p.words), dev)
+        if p.words < 1:
+            raise ValueError("mask must have at least one word")
+    if idx is not None:
+        (_, _, p.k), _ = _first(idx, "idx", _I32, 3)
+        p.idx = _arg(idx, "idx", _I32, (S, N, p.k), dev)
+        if p.k < 1:
+            raise ValueError("idx must have at least one column")
+    return p
+
+
+def tree_attention(q, prefix, table, page, C, sm_scale, c_scale=None, rope=None, mask=None, idx=None, longest=0,
+                   with_lse=False, ws=None, out=None):
+    """Latent attention (absorbed form) of N drafted tokens in each of S
+    sequences, q [S, N, H, 576], over a paged latent cache (table and page: see
+    paged_append; C, c_scale, rope: see make_cache). Every token sees the
+    prefix[s] int32 committed tokens of its sequence, or those of them that idx
+    [S, N, k] int32 names (positions, -1: none), and of the drafted ones, which
+    follow at positions prefix[s] + b, those whose bit b its mask has: int64 [S, N]
+    or [S, N, words], itself and its ancestors; without masks itself and those
+    before it. A mask of 0 (or a prefix below 0) marks padding: zeros, -inf.
+    longest: the length that the call is planned for (results do not depend on
+    it). The result carries no gradient (it is detached from q and the cache)."""
+    p = make_tree_problem(q, prefix, table, page, C, sm_scale, c_scale, rope, mask, idx, longest)
+    return _attention(lib().misa_tree_attention, lib().misa_tree_workspace_bytes, p, q, LATENT, with_lse, ws, out)
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, coded=False, group=0, out=None, out_sum=None):
+    """Root-mean-square norm of rows x [n, width] bfloat16 (rows may be strided),
+    x + residual where residual [n, width] is given: y [n, width] bfloat16, or
+    (coded) E4M3FN codes and their scales, float32 [n] or (group=128) [n,
+    ceil(width / 128)]; with a residual the sum in bfloat16 follows. out (the
+    bfloat16 result, or codes and scales) and out_sum (which may be residual) are
+    written if given. The results carry no gradient."""
+    if x is None or x.dim() != 2:
+        raise ValueError("x must be rows [n, width]")
+    width = x.shape[1]
+    dev = x.get_device()
+    at, n, ld = _rows(x, "x", width, dev)
+    w_at, w_dtype = _weight(weight, width, dev)
+    res = None if residual is None else _arg(residual, "residual", _BF16, (n, width), dev)
+    if out_sum is not None and residual is None:
+        raise ValueError("out_sum is only for a residual")
+    p = NormProblem(n, width, at, ld, res, w_at, w_dtype, 1 if coded else 0, group, eps)
+    y, scale = out if coded and out is not None else (out, None)
+    shape = (n, -(-width // 128)) if group else (n,)
+    if y is None:
+        y = x.new_empty((n, width), dtype=torch.float8_e4m3fn if coded else torch.bfloat16)
+        scale = x.new_empty(shape, dtype=torch.float32) if coded else None
+    y_at = _arg(y, "out", _CODES if coded else _BF16, (n, width), dev)
+    s_at = _arg(scale, "scale", _F32, shape, dev) if coded else None
+    total = out_sum if residual is None or out_sum is not None else x.new_empty((n, width), dtype=torch.bfloat16)
+    t_at = None if total is None else _arg(total, "out_sum", _BF16, (n, width), dev)
+    _on(dev, lib().misa_rms_norm, p, y_at, s_at, t_at)
+    got = ((y, scale) if coded else (y,)) + (() if total is None else (total,))
+    return got if len(got) > 1 else y
 
 
 def profile_enable(on: bool = True):

@@ -16,7 +16,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmisa.so")
 PROBE_LIB = os.path.join(HERE, "libmisa_probe.so")  # benchmark's streaming-floor probe
 SOURCES = ["route_kernels.hip", "route_fast.hip", "score_kernels.hip", "topk_kernels.hip", "api.hip",
-           "cache_kernels.hip", "latent_kernels.hip", "expanded_kernels.hip", "api_attention.hip"]
+           "cache_kernels.hip", "latent_kernels.hip", "expanded_kernels.hip", "api_attention.hip",
+           "norm_kernels.hip", "paged_kernels.hip", "tree_kernels.hip", "api_paged.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = [
@@ -33,7 +34,8 @@ CFLAGS = [
 # stay in private memory
 EXTRA = {"score_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "latent_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"],
-         "expanded_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"]}
+         "expanded_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"],
+         "tree_kernels.hip": ["-mllvm", "-disable-promote-alloca-to-lds"]}
 
 
 def _compile(src: str) -> str:

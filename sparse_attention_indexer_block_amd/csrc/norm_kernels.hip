@@ -1,0 +1,118 @@
+// Root-mean-square norm of rows, with the addition of a residual before it and, if
+// asked for, a result coded to E4M3FN with a scale for each row or each 128 columns:
+//
+//   h = x + residual,  sum = h in bf16,  y = (h / sqrt(mean(h^2) + eps)) * weight
+//
+// h, y and the scales are formed in fp32 and each result is rounded once.
+#include "attention.h"
+#include "row_device.h"
+
+namespace misa {
+
+// W waves a row, CH chunks of eight values a lane (chunk = thread + 64 W i); a
+// workgroup of four waves takes 4 / W rows, or one of more waves. A row is read once
+// and stays in registers.
+template <int W, int CH, NormOut OUT>
+__global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_rms_norm(NormArgs p) {
+  constexpr int ROWS = W > 4 ? 1 : 4 / W, TPR = 64 * W;
+  __shared__ double sums[ROWS * W];
+  __shared__ uint32_t tops[ROWS * W];
+  const int tid = threadIdx.x, lane = tid & 63, in_row = tid % TPR, rr = tid / TPR, wave = tid / 64;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + rr;
+  const bool live = row < p.n;
+  const int64_t r = live ? row : p.n - 1;
+  const int chunks = p.width / 8;
+  u32x4 vx[CH], vr[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = min(in_row + TPR * i, chunks - 1);
+    vx[i] = *reinterpret_cast<const u32x4*>(p.x + r * p.x_ld + c * 8);
+    if (p.residual) vr[i] = *reinterpret_cast<const u32x4*>(p.residual + r * p.width + c * 8);
+  }
+  float h[CH][8];
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = in_row + TPR * i;
+    unpack8(vx[i], h[i]);
+    if (p.residual) {
+      float b[8];
+      unpack8(vr[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] += b[j];
+    }
+    if (c < chunks) {
+      sum = squares(h[i], sum);
+      if (p.sum && live) *reinterpret_cast<u32x4*>(p.sum + row * p.width + c * 8) = pack8(h[i]);
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  if constexpr (W > 1) {
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) sum += sums[rr * W + i];
+  }
+  const float inv = inverse_rms(sum, p.width, p.eps);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = in_row + TPR * i;
+    float w[8];
+    load_weights(p.weight, p.weight_f32, min(c, chunks - 1) * 8, w);
+    scale_row(h[i], inv, w);
+    if constexpr (OUT == NormOut::kBf16) {
+      if (c < chunks && live) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.y) + row * p.width + c * 8) = pack8(h[i]);
+    } else if constexpr (OUT == NormOut::kGroupCodes) {
+      const RowCode code(max_of_16(c < chunks ? magnitude_bits(h[i]) : 0u));
+      if (c < chunks && live) {
+        *reinterpret_cast<u32x2*>(static_cast<unsigned char*>(p.y) + row * p.width + c * 8) = code.eight(h[i]);
+        if ((lane & 15) == 0) p.scale[row * ((chunks + 15) / 16) + c / 16] = code.scale;
+      }
+    } else {
+      if (c < chunks) top = max(top, magnitude_bits(h[i]));
+    }
+  }
+  if constexpr (OUT == NormOut::kRowCodes) {
+    top = wave_max_u32(top);
+    if constexpr (W > 1) {
+      if (lane == 0) tops[wave] = top;
+      __syncthreads();
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) top = max(top, tops[rr * W + i]);
+    }
+    const RowCode code(top);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = in_row + TPR * i;
+      if (c < chunks) *reinterpret_cast<u32x2*>(static_cast<unsigned char*>(p.y) + row * p.width + c * 8) = code.eight(h[i]);
+    }
+    if (in_row == 0) p.scale[row] = code.scale;
+  }
+}
+
+template <int W, int CH>
+static hipError_t norm_as(const LaunchCtx& cx, const NormArgs& a, NormOut out) {
+  constexpr int ROWS = W > 4 ? 1 : 4 / W;
+  const dim3 grid((unsigned)(((int64_t)a.n + ROWS - 1) / ROWS)), block(W > 4 ? 64 * W : 256);
+  switch (out) {
+    case NormOut::kBf16: return cx.launch("k_rms_norm", k_rms_norm<W, CH, NormOut::kBf16>, grid, block, 0, a);
+    case NormOut::kRowCodes: return cx.launch("k_rms_norm", k_rms_norm<W, CH, NormOut::kRowCodes>, grid, block, 0, a);
+    default: return cx.launch("k_rms_norm", k_rms_norm<W, CH, NormOut::kGroupCodes>, grid, block, 0, a);
+  }
+}
+
+// A wave for a row of up to 512 values, otherwise four.
+hipError_t launch_rms_norm(const LaunchCtx& cx, const NormArgs& a, NormOut out) {
+  if (a.width <= 512) return norm_as<1, 1>(cx, a, out);
+  if (a.width <= 2048) return norm_as<4, 1>(cx, a, out);
+  if (a.width <= 4096) return norm_as<4, 2>(cx, a, out);
+  if (a.width <= 8192) return norm_as<4, 4>(cx, a, out);
+  return norm_as<8, 4>(cx, a, out);
+}
+
+}  // namespace misa
