@@ -421,7 +421,7 @@ def _first(t, name: str, dtypes, dims: int):
 
 def _on(dev: int, call, *args):
     """call(*args, current stream of GPU dev) with dev as the current GPU."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:  # (a tensor of GPU dev exists: the GPUs are initialised)
         status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -547,7 +547,7 @@ _I64, _WEIGHT = (torch.int64,), (torch.bfloat16, torch.int16, torch.float32)
 
 
 def _pages(table, page, dev) -> Pages:
-    (seqs, per), _ = _first(table, "table", _I32, 2)
+    seqs, per = table.shape if table is not None and table.dim() == 2 else _first(table, "table", _I32, 2)[0]
     return Pages(_arg(table, "table", _I32, (seqs, per), dev), seqs, per, page)
 
 
@@ -557,20 +557,21 @@ def _weight(weight, width, dev):
 
 
 def _rotation(rot, pairs, dev) -> Rotation:
-    (positions, _), _ = _first(rot, "rot", _F32, 2)
+    positions = rot.shape[0] if rot is not None and rot.dim() else 0
     return Rotation(_arg(rot, "rot", _F32, (positions, ROTARY), dev), positions, 1 if pairs else 0)
 
 
 def _rows(x, name: str, width: int, dev: int):
     """Address, count and distance of rows x [n, width] bfloat16 that may be columns of wider ones."""
-    if x is None or not x.is_cuda or x.dtype not in _BF16 or x.get_device() != dev or x.dim() != 2 or x.shape[1] != width:
+    if x is None or x.dtype not in _BF16 or not x.is_cuda or x.get_device() != dev or x.dim() != 2 or x.shape[1] != width:
         _refuse(x, name, _BF16, ("n", width), dev)
+    n = x.shape[0]
     ld, inner = x.stride()
-    if x.shape[0] <= 1:
+    if n <= 1:
         ld = width
     if (inner != 1 and width > 1) or ld < width:
         raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
-    return x.data_ptr(), x.shape[0], ld
+    return x.data_ptr(), n, ld
 
 
 def paged_append(x, seq, pos, table, page, C, c_scale=None, rope=None, weight=None, eps=1e-6, rot=None, turn=None,
@@ -586,21 +587,23 @@ def paged_append(x, seq, pos, table, page, C, c_scale=None, rope=None, weight=No
     instead of values 32 apart. Rows that name no place (pos or seq of -1, say)
     write nothing; the others must name distinct ones."""
     c = make_cache(C, c_scale, rope)
-    dev = C.get_device()
-    at, n, ld = _rows(x, "x", c.d + c.dr, dev)
-    p = AppendProblem(n, at, ld, _arg(seq, "seq", _I32, (n,), dev), _arg(pos, "pos", _I32, (n,), dev),
-                      None if turn is None else _arg(turn, "turn", _I32, (n,), dev))
+    dev, d, dr = C.get_device(), c.d, c.dr
+    at, n, ld = _rows(x, "x", d + dr, dev)
+    w_at = w_dtype = 0
     if weight is not None:
-        p.weight, p.w_dtype = _weight(weight, c.d, dev)
-        p.eps = eps
+        w_at, w_dtype = _weight(weight, d, dev)
     if rot is not None:
-        p.rotation = _rotation(rot, pairs, dev)
-        p.rot_at = rot_at if rot_at is not None else c.d if c.dr else 0
+        turning = _rotation(rot, pairs, dev)
+        if rot_at is None:
+            rot_at = d if dr else 0
     elif rot_at is not None or pairs:
         raise ValueError("rot_at and pairs are only for a rotation (rot)")
-    p.pages = _pages(table, page, dev)
-    p.cache = c
-    _on(dev, lib().misa_paged_append, p)
+    else:
+        turning, rot_at = Rotation(), 0
+    _on(dev, lib().misa_paged_append, AppendProblem(
+        n, at, ld, _arg(seq, "seq", _I32, (n,), dev), _arg(pos, "pos", _I32, (n,), dev),
+        None if turn is None else _arg(turn, "turn", _I32, (n,), dev), w_at, w_dtype, rot_at, eps, turning,
+        _pages(table, page, dev), c))
 
 
 def _heads(x, name: str, T, H, dev: int):
@@ -679,26 +682,37 @@ def rms_norm(x, weight, eps=1e-6, residual=None, coded=False, group=0, out=None,
     written if given. The results carry no gradient."""
     if x is None or x.dim() != 2:
         raise ValueError("x must be rows [n, width]")
-    width = x.shape[1]
-    dev = x.get_device()
+    width, dev = x.shape[1], x.get_device()
     at, n, ld = _rows(x, "x", width, dev)
     w_at, w_dtype = _weight(weight, width, dev)
-    res = None if residual is None else _arg(residual, "residual", _BF16, (n, width), dev)
-    if out_sum is not None and residual is None:
+    shape = (n, width)
+    p = NormProblem(n, width, at, ld, None, w_at, w_dtype, 1 if coded else 0, group, eps)
+    t_at = s_at = None
+    if residual is not None:
+        p.residual = _arg(residual, "residual", _BF16, shape, dev)
+        if out_sum is None:
+            out_sum = torch.empty_like(x, dtype=torch.bfloat16)  # (strided rows give contiguous ones)
+            t_at = out_sum.data_ptr()
+        else:
+            t_at = _arg(out_sum, "out_sum", _BF16, shape, dev)
+    elif out_sum is not None:
         raise ValueError("out_sum is only for a residual")
-    p = NormProblem(n, width, at, ld, res, w_at, w_dtype, 1 if coded else 0, group, eps)
-    y, scale = out if coded and out is not None else (out, None)
-    shape = (n, -(-width // 128)) if group else (n,)
-    if y is None:
-        y = x.new_empty((n, width), dtype=torch.float8_e4m3fn if coded else torch.bfloat16)
-        scale = x.new_empty(shape, dtype=torch.float32) if coded else None
-    y_at = _arg(y, "out", _CODES if coded else _BF16, (n, width), dev)
-    s_at = _arg(scale, "scale", _F32, shape, dev) if coded else None
-    total = out_sum if residual is None or out_sum is not None else x.new_empty((n, width), dtype=torch.bfloat16)
-    t_at = None if total is None else _arg(total, "out_sum", _BF16, (n, width), dev)
+    scales = (n, -(-width // 128)) if group else (n,)
+    if out is None:
+        y = torch.empty_like(x, dtype=torch.float8_e4m3fn if coded else torch.bfloat16)
+        y_at = y.data_ptr()
+        if coded:
+            scale = x.new_empty(scales, dtype=torch.float32)
+            s_at = scale.data_ptr()
+    else:
+        y, scale = out if coded else (out, None)
+        y_at = _arg(y, "out", _CODES if coded else _BF16, shape, dev)
+        if coded:
+            s_at = _arg(scale, "scale", _F32, scales, dev)
     _on(dev, lib().misa_rms_norm, p, y_at, s_at, t_at)
-    got = ((y, scale) if coded else (y,)) + (() if total is None else (total,))
-    return got if len(got) > 1 else y
+    if coded:
+        return (y, scale) if residual is None else (y, scale, out_sum)
+    return y if residual is None else (y, out_sum)
 
 
 def profile_enable(on: bool = True):

@@ -101,8 +101,9 @@ struct AppendArgs {
   double eps;
   Rotation rot;          // rot null: no rotation
   int32_t rot_at;        // first rotated column
+  double inv_width;      // (set by the launcher) 1 / d
 };
-hipError_t launch_paged_append(const LaunchCtx& cx, const AppendArgs& a, bool fp8);
+hipError_t launch_paged_append(const LaunchCtx& cx, AppendArgs a, bool fp8);
 struct RotateArgs {
   int32_t T, H;
   const uint16_t* x;     // [T, H, 64], rows x_h and queries x_t elements apart
@@ -123,12 +124,13 @@ struct NormArgs {
   const void* weight;        // [width]
   bool weight_f32;
   double eps;
+  double inv_width;          // (set by the launcher) 1 / width
   void* y;                   // [n, width] bf16 or codes
   float* scale;              // [n] or [n, ceil(width / 128)] (codes)
   uint16_t* sum;             // [n, width] or null
 };
 enum class NormOut { kBf16, kRowCodes, kGroupCodes };
-hipError_t launch_rms_norm(const LaunchCtx& cx, const NormArgs& a, NormOut out);
+hipError_t launch_rms_norm(const LaunchCtx& cx, NormArgs a, NormOut out);
 
 // ---- attention of drafted tokens (tree_kernels.hip)
 struct TreeArgs : LatentArgs {

@@ -23,11 +23,13 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_rms_norm(NormArgs p) {
   const int64_t r = live ? row : p.n - 1;
   const int chunks = p.width / 8;
   u32x4 vx[CH], vr[CH];
+  float w[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = min(in_row + TPR * i, chunks - 1);
     vx[i] = *reinterpret_cast<const u32x4*>(p.x + r * p.x_ld + c * 8);
     if (p.residual) vr[i] = *reinterpret_cast<const u32x4*>(p.residual + r * p.width + c * 8);
+    if constexpr (CH <= 2) load_weights(p.weight, p.weight_f32, c * 8, w[i]);  // (more would not fit beside a row's values)
   }
   float h[CH][8];
   double sum = 0.0;
@@ -46,8 +48,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_rms_norm(NormArgs p) {
       if (p.sum && live) *reinterpret_cast<u32x4*>(p.sum + row * p.width + c * 8) = pack8(h[i]);
     }
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  sum = sum_of<64>(sum);
   if constexpr (W > 1) {
     if (lane == 0) sums[wave] = sum;
     __syncthreads();
@@ -55,14 +56,13 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_rms_norm(NormArgs p) {
 #pragma unroll
     for (int i = 0; i < W; ++i) sum += sums[rr * W + i];
   }
-  const float inv = inverse_rms(sum, p.width, p.eps);
+  const float inv = inverse_rms(sum, p.inv_width, p.eps);
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = in_row + TPR * i;
-    float w[8];
-    load_weights(p.weight, p.weight_f32, min(c, chunks - 1) * 8, w);
-    scale_row(h[i], inv, w);
+    if constexpr (CH > 2) load_weights(p.weight, p.weight_f32, min(c, chunks - 1) * 8, w[i]);
+    scale_row(h[i], inv, w[i]);
     if constexpr (OUT == NormOut::kBf16) {
       if (c < chunks && live) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.y) + row * p.width + c * 8) = pack8(h[i]);
     } else if constexpr (OUT == NormOut::kGroupCodes) {
@@ -107,7 +107,8 @@ static hipError_t norm_as(const LaunchCtx& cx, const NormArgs& a, NormOut out) {
 }
 
 // A wave for a row of up to 512 values, otherwise four.
-hipError_t launch_rms_norm(const LaunchCtx& cx, const NormArgs& a, NormOut out) {
+hipError_t launch_rms_norm(const LaunchCtx& cx, NormArgs a, NormOut out) {
+  a.inv_width = 1.0 / a.width;
   if (a.width <= 512) return norm_as<1, 1>(cx, a, out);
   if (a.width <= 2048) return norm_as<4, 1>(cx, a, out);
   if (a.width <= 4096) return norm_as<4, 2>(cx, a, out);

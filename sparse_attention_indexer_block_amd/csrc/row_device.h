@@ -75,8 +75,41 @@ __device__ __forceinline__ double squares(const float (&x)[8], double sum) {
   for (int i = 0; i < 8; ++i) sum = fma((double)x[i], (double)x[i], sum);
   return sum;
 }
-__device__ __forceinline__ float inverse_rms(double sum, int width, double eps) {
-  return (float)(1.0 / sqrt(sum / width + eps));
+// 1 / sqrt(sum * inv_width + eps): the hardware's estimate and two steps of Newton's method,
+// which leave it within a few 2^-53, then one rounding. (Library division and root take
+// some hundred instructions, which a row's whole workgroup would wait for.)
+__device__ __forceinline__ float inverse_rms(double sum, double inv_width, double eps) {
+  const double a = fma(sum, inv_width, eps);
+  double y = __builtin_amdgcn_rsq(a);
+  const double first = y;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = fma(y, fma(-0.5 * a * y, y, 0.5), y);
+  return (float)(a > 0.0 && a < (double)INFINITY ? y : first);  // (0 and infinity are exact)
+}
+// Sum over groups of LANES (16 or 64) lanes, in every lane.
+template <int LANES>
+__device__ __forceinline__ double sum_of(double v) {
+  auto step = [&](auto move) {
+    const u32x2 b = __builtin_bit_cast(u32x2, v);
+    v += __builtin_bit_cast(double, u32x2{move(b.x), move(b.y)});
+  };
+  step([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, false); });  // row_ror:8
+  step([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xf, 0xf, false); });  // row_ror:4
+  step([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xf, 0xf, false); });  // row_ror:2
+  step([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xf, 0xf, false); });  // row_ror:1
+  if constexpr (LANES == 64) {
+    auto lane = [&](int i) {
+      const u32x2 b = __builtin_bit_cast(u32x2, v);
+      return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)b.x, i), (uint32_t)__builtin_amdgcn_readlane((int)b.y, i)});
+    };
+    v = (lane(0) + lane(16)) + (lane(32) + lane(48));
+  }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  if constexpr (LANES == 64) return wave_max_u32(v);
+  return max_of_16(v);
 }
 __device__ __forceinline__ void scale_row(float (&x)[8], float r, const float (&w)[8]) {
 #pragma clang fp contract(off)
