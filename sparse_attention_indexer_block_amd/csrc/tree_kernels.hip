@@ -10,7 +10,7 @@
 // shared out.
 #include <algorithm>
 
-#include "latent_device.h"
+#include "latent_pair.h"
 
 namespace misa {
 
@@ -44,9 +44,10 @@ struct TreeWork {
     int rows, node, i;     // rows (0: none), node, unit of the row tile
     bool live;             // not padding
   };
-  __device__ __forceinline__ Unit unit(int i) const {
+  __device__ __forceinline__ Unit unit(int i) const { return unit_of(i, r); }
+  __device__ __forceinline__ Unit unit_of(int i, int tile) const {
     const int hc = (p.H + U - 1) / U;
-    const int g = r * kUnits + i, node = g / hc, c = g % hc;
+    const int g = tile * kUnits + i, node = g / hc, c = g % hc;
     Unit u{0, 0, 0, i, false};
     if (node >= p.N) return u;
     u.row = ((int64_t)s * p.N + node) * p.H + c * U;
@@ -55,15 +56,23 @@ struct TreeWork {
     u.live = !padded;
     if (p.mask && u.live) {
       uint64_t any = 0;
-      for (int w = 0; w < p.words; ++w) any |= p.mask[((int64_t)s * p.N + node) * p.words + w];
+      for (int w = 0; w < p.words; ++w) any |= mask_word(node, w);
       u.live = any != 0;
     }
     return u;
   }
+  // Word w of the node's mask, the same for all lanes. It has landed where this ends: where
+  // paths with and without a load meet, the compiler would wait for copies in flight.
+  __device__ __forceinline__ uint64_t mask_word(int node, int w) const {
+    uint64_t x = p.mask[((int64_t)s * p.N + node) * p.words + w];
+    asm volatile("" : "+v"(x));
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+  }
   // which positions of tile ti (at or past np) the node sees
   __device__ __forceinline__ uint64_t bits(int node, int ti) const {
     const int w = ti - np;
-    if (p.mask) return p.mask[((int64_t)s * p.N + node) * p.words + w];
+    if (p.mask) return mask_word(node, w);
     const int n = node + 1 - 64 * w;
     return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
   }
@@ -190,9 +199,10 @@ struct TreeWork {
   // its page, or one past the table's end for it (row_at knows). A load without a
   // branch: it is asked for a tile ahead, and a branch around it would wait for
   // what is in flight.
-  __device__ __forceinline__ int list_entry(int ti) const {
-    return p.pages.table[(int64_t)s * p.pages.per + min(position(ti) >> p.pages.page_log2, p.pages.per - 1)];
+  __device__ __forceinline__ const int32_t* entry_at(int ti) const {
+    return p.pages.table + (int64_t)s * p.pages.per + min(position(ti) >> p.pages.page_log2, p.pages.per - 1);
   }
+  __device__ __forceinline__ int list_entry(int ti) const { return *entry_at(ti); }
   __device__ __forceinline__ int list_after(int ti, int next, int v) const {
     asm volatile("" : "+v"(v));
     if (next != ti + 1) {
@@ -203,9 +213,14 @@ struct TreeWork {
   }
   // the cache row of key 64 * ti + lane in page v, or -1; a committed one, or a position of a mask's word
   __device__ __forceinline__ int row_at(int ti, int v) const {
-    const int j = position(ti), lg = p.pages.page_log2;
-    const int64_t row = ((int64_t)v << lg) + (j & ((1 << lg) - 1));
-    return ((ti >= np || j < prefix) && v >= 0 && (j >> lg) < p.pages.per && row < p.rows) ? (int)row : -1;
+    return (position(ti) >> p.pages.page_log2) < p.pages.per ? row_in(ti, v, position(ti)) : -1;
+  }
+  // the same for a tile below np, whose positions the table has
+  __device__ __forceinline__ int plain_row(int ti, int v) const { return row_in(ti, v, ti * kAttnTile + lane); }
+  __device__ __forceinline__ int row_in(int ti, int v, int j) const {
+    const int lg = p.pages.page_log2, pages = (p.rows + (1 << lg) - 1) >> lg;
+    const int row = (int)((uint32_t)v << lg) + (j & ((1 << lg) - 1));  // (below 2^31 if v is a page)
+    return (ti >= np || j < prefix) && (uint32_t)v < (uint32_t)pages && row < p.rows ? row : -1;
   }
   // the same, if any unit sees it
   __device__ __forceinline__ int row_of(int ti, int v) const {
@@ -236,10 +251,15 @@ struct TreeWork {
   // The wide kernel's walk: a tile of a word is taken once for all units if they
   // see the same of it, otherwise once for each kind (who: the unit it is of).
   __device__ __forceinline__ int next_pass(int ti, int who, int v, int& who_next, int& rows) const {
+    // (what follows of the units is rare; it is formed here, not kept from before the loop)
+    const int tile = __builtin_amdgcn_readfirstlane(anew(r));
     bool asked = who < 0;  // v is tile ti's
     ++who;
     for (; ti < tile_end; ++ti, who = 0) {
-      if (!asked) v = list_entry(ti);
+      if (!asked) {
+        v = list_entry(ti);
+        asm volatile("" : "+v"(v));  // (waited for here, not where the paths meet)
+      }
       asked = false;
       const int row = row_at(ti, v);
       if (ti < np) {
@@ -253,7 +273,7 @@ struct TreeWork {
       int first = -1;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const Unit u = unit(i);
+        const Unit u = unit_of(i, tile);
         live[i] = u.live;
         b[i] = u.live ? bits(u.node, ti) : 0ull;
         if (u.live && first < 0) first = i;
@@ -460,7 +480,7 @@ static hipError_t launch_tree_t(const LaunchCtx& cx, const TreeArgs& a, int nq, 
     case 16: return cx.launch("k_tree_16", k_latent<16, FP8, TreeForm>, grid, dim3(256), 0, a);
     case 32: return cx.launch("k_tree_32", k_latent<32, FP8, TreeForm>, grid, dim3(256), 0, a);
     case 64: return cx.launch("k_tree_64", k_latent_wide<2, FP8, TreeForm>, grid, dim3(256), 0, a);
-    default: return cx.launch("k_tree_128", k_latent_wide<4, FP8, TreeForm>, grid, dim3(256), 0, a);
+    default: return cx.launch("k_tree_128", k_latent_pair<FP8, TreeForm>, grid, dim3(256), 0, a);
   }
 }
 
