@@ -143,7 +143,7 @@ struct TreeArgs : LatentArgs {
   int32_t tiles_a_seq;    // row tiles of a sequence
   int32_t budget[2];      // splits over all sequences, in either of two cuts
   int32_t least;          // tiles a split takes at least
-  float fixed, tile;      // what a workgroup and a tile cost (us)
+  float fixed, tile, join;  // what a workgroup, a tile and the join of a split cost (us)
   int32_t* rec;           // [seqs, 2]: first slot and splits of a sequence
 };
 struct TreePlan {

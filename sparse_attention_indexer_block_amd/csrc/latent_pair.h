@@ -90,21 +90,28 @@ struct PairLds {
 //   - the next step's scores run beside this one's softmax, the copies three steps ahead
 //     beside the values' products, the reads of LDS ahead of both.
 // A second wave a SIMD to issue beside does not fit: 256 sums and 144 of queries a lane.
-// 2 sequences x 64 tokens x 128 heads over 32,000 keys, bf16: 921 us, 1.24 PFLOP/s (a
-// library's product of 8192^3 reaches 1.32); k_latent_wide 1060. 24 sequences x 4 tokens x 128
-// heads, up to 8000 keys each, codes: 182 us, 203. A step takes some 3700 cycles: 1480 of
-// scores (codes: 2360, bound by the issue of 192 conversions), 2070 of values, of which copies
-// cost 470 (the address arithmetic of the rotary rows 160), the wait for the partner's
-// rescaling 160.
-// Tried and left: two barriers a step (960 us), copies spread over scores and values (928),
-// four stages of rotary rows (no room), values' operands shared by four waves (LDS as the
-// bound).
+// 2 sequences x 64 tokens x 128 heads over 32,000 keys, bf16: 893 us, 1.28 PFLOP/s (a
+// library's product of 8192^3 reaches 1.32, and the clock falls as the kernel gains: the
+// last step took 9 % of its cycles and 2.4 % of its time); k_latent_wide 1060. A step of 32
+// keys: 70 cycles until the scores, 1670 with them, 1670 of values. With codes 85, 2550 and
+// 1860: the issue of 192 conversions bounds the scores. A workgroup's rest, some 45,000
+// cycles: 10,000 to find its share, 9,000 for the queries, 9,000 until the first scores are
+// there, 18,000 for its partial sums.
+// Tried and left: two barriers a step (960 us), copies spread over scores and values (928
+// beside 921), four stages of rotary rows (no room), values' operands shared by four waves
+// (bound by LDS).
 template <bool FP8, class Form>
 __global__ __launch_bounds__(256, 1) void k_latent_pair(typename Form::Args p) {
   using Lds = PairLds<FP8>;
   constexpr int kStride = FP8 ? kLatent : 2 * (kLatent + kRotary);     // bytes of a cache row
   constexpr int kCopies = FP8 ? 6 : 9;                                 // of a wave and step
   constexpr int kKeyReads = FP8 ? 20 : 36, kAhead = FP8 ? 4 : 6, kAheadV = FP8 ? 4 : 3;
+  // The waves meet where the weights are done, well before the values, so that the partner's
+  // are there when the values begin. With codes no registers are left to hold them through
+  // the scores (8 would spill in the loop; 186 us became 192): there the waves meet behind the
+  // scores, and the partner's products run two behind the own ones, while its weights come.
+  constexpr bool kEarly = !FP8;
+  constexpr int kLag = kEarly ? 0 : 2;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Lds::kBytes];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -401,9 +408,20 @@ __global__ __launch_bounds__(256, 1) void k_latent_pair(typename Form::Args p) {
       for (int e = 0; e < 16; ++e) s[e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? s[e] : -INFINITY;
     }
     float top, f = 1.f;
-    bf16x8 pb[2];
+    bf16x8 pb[2], po[2];
+    float fo;
     f32x4 sc;
     u32x4 vring[kAheadV];
+    // What was copied in the last step has landed, and this one's weights are there. One
+    // barrier a step: behind it all waves are done with the last step's values, whose place
+    // this step's copies take, and with what they handed each other the step before that.
+    auto meet = [&]() __attribute__((always_inline)) {
+      wait_copies();
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) po[j] = lds_read<bf16x8>(weights(N, w ^ 1) + j * 1024);
+      fo = lds_read<float>(factors(N, w ^ 1));
+    };
     auto work = [&](auto number) __attribute__((always_inline)) {
       constexpr int t = decltype(number)::value;
       if constexpr (t < 4) {
@@ -437,30 +455,22 @@ __global__ __launch_bounds__(256, 1) void k_latent_pair(typename Form::Args p) {
         *(__attribute__((address_space(3))) bf16x8*)(uintptr_t)(weights(N, w) + (t - 22) * 1024) = pb[t - 22];
       } else if constexpr (t == 24) {
         *(__attribute__((address_space(3))) float*)(uintptr_t)factors(N, w) = f;
+      } else if constexpr (kEarly && t == 26) {
+        meet();
       } else if constexpr (t >= 36 - kAheadV) {
         vring[t - (36 - kAheadV)] = read_value(N, t - (36 - kAheadV));
       }
     };
     score(s_next, next, third_next, std::integral_constant<int, 1 - N>{}, work);
-    // What was copied in the last step has landed, and this one's weights are there. One
-    // barrier a step: behind it all waves are done with the last step's values, whose place
-    // this step's copies take, and with what they handed each other the step before that.
-    wait_copies();
-    lds_barrier();
-
-    bf16x8 po[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) po[j] = lds_read<bf16x8>(weights(N, w ^ 1) + j * 1024);
-    const float fo = lds_read<float>(factors(N, w ^ 1));
+    if constexpr (!kEarly) meet();
     int entry = 0;
-    // the own rows' products run ahead of the partner's, whose weights are on their way
-    each<16 + 2>([&](auto number) __attribute__((always_inline)) {
+    each<16 + kLag>([&](auto number) __attribute__((always_inline)) {
       constexpr int i = decltype(number)::value;
       if constexpr (i < 16) {
         const bf16x8 a = operand(vring[i % kAheadV]);
         own[i & 7] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(PART ? seen_by(a, cur.own) : a, pb[i >> 3], own[i & 7], 0, 0, 0);
       }
-      if constexpr (i == 1) {
+      if constexpr (i == kLag / 2) {
         if (__builtin_expect(__any(fo != 1.f), 0)) {
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
@@ -488,15 +498,16 @@ __global__ __launch_bounds__(256, 1) void k_latent_pair(typename Form::Args p) {
         }
       }
       if constexpr (i == 14) begin_copies(N == 0 ? 0 : 1);  // of the next step
-      if constexpr (i >= 2) {
-        constexpr int k = i - 2;
+      if constexpr (i >= kLag) {
+        constexpr int k = i - kLag;
         const bf16x8 a = operand(vring[k % kAheadV]);
         oth[k & 7] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(PART ? seen_by(a, cur.other) : a, po[k >> 3], oth[k & 7], 0, 0, 0);
         if constexpr (k + kAheadV < 16) vring[k % kAheadV] = read_value(N, k + kAheadV);
         // the next step's first reads come last
-        if constexpr (k >= 12) {  // (behind the step to the next pair)
+        constexpr int kLast = 2 + kLag;
+        if constexpr (i >= 14) {  // (behind the step to the next pair)
 #pragma unroll
-          for (int x = (k - 12) * kAhead / 4; x < (k - 11) * kAhead / 4; ++x) ring[x] = read_key(0u, N, x);
+          for (int x = (i - 14) * kAhead / kLast; x < (i - 13) * kAhead / kLast; ++x) ring[x] = read_key(0u, N, x);
         }
       }
       __builtin_amdgcn_sched_barrier(0);

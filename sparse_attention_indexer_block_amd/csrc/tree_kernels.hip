@@ -26,7 +26,8 @@ constexpr int kPlanSeqs = 256;
 // max(1, ceil(n / c)) of them, and c is the smallest (to within a 32nd of its range)
 // whose splits fit the budget. Two budgets are held against each other, one of which
 // fills the card once more: it pays where lengths differ, since the longest sequence
-// is cut and not the others.
+// is cut and not the others, and costs twice the partial sums to join (24 sequences of up
+// to 8000 keys, 4 tokens x 128 heads, codes: splits of 37 tiles 198 us, of 16 206).
 template <int NQ, int U>
 struct TreeWork {
   const TreeArgs& p;
@@ -37,6 +38,7 @@ struct TreeWork {
   int slot, splits;        // the split's place among all sequences' splits; splits of this sequence
   int cur, tile_end;
   bool valid;
+  uint32_t alive;          // bit i: unit i is not padding
   static constexpr int kUnits = NQ / U;
 
   struct Unit {
@@ -53,12 +55,7 @@ struct TreeWork {
     u.row = ((int64_t)s * p.N + node) * p.H + c * U;
     u.rows = min(U, p.H - c * U);
     u.node = node;
-    u.live = !padded;
-    if (p.mask && u.live) {
-      uint64_t any = 0;
-      for (int w = 0; w < p.words; ++w) any |= mask_word(node, w);
-      u.live = any != 0;
-    }
+    u.live = alive >> i & 1;
     return u;
   }
   // Word w of the node's mask, the same for all lanes. It has landed where this ends: where
@@ -94,23 +91,24 @@ struct TreeWork {
     int c, slots;
   };
   // (lane l holds the tiles of sequences l, l + 64, ...; -1: no sequence)
-  static __device__ __forceinline__ int slots_of(const int (&n)[kPlanSeqs / 64], int c) {
+  static __device__ __forceinline__ int slots_of(const int (&n)[kPlanSeqs / 64], int seqs, int c) {
     const float inv = 1.f / (float)c;
     int m = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanSeqs / 64; ++i) m += n[i] < 0 ? 0 : max(1, shares(n[i], c, inv));
+    for (int i = 0; i < kPlanSeqs / 64; ++i)
+      if (64 * i < seqs) m += n[i] < 0 ? 0 : max(1, shares(n[i], c, inv));
     return (int)wave_total_u32((uint32_t)m);
   }
   static __device__ __forceinline__ Cut cut(const int (&n)[kPlanSeqs / 64], int total, int most, int seqs, int budget, int least) {
     int lo = max(least, (total + budget - 1) / budget);
     int hi = budget > seqs ? min(most, (total + budget - seqs - 1) / (budget - seqs)) : most;
-    int at = slots_of(n, lo);
+    int at = slots_of(n, seqs, lo);
     if (at <= budget) return {lo, at};
     // lo's splits do not fit, hi's do: sum of ceil(n / c) < total / c + seqs
-    at = slots_of(n, hi);
+    at = slots_of(n, seqs, hi);
 #pragma unroll 1
     for (int i = 0; i < 5 && hi - lo > 1; ++i) {
-      const int mid = (lo + hi) / 2, k = slots_of(n, mid);
+      const int mid = (lo + hi) / 2, k = slots_of(n, seqs, mid);
       if (k <= budget) hi = mid, at = k;
       else lo = mid;
     }
@@ -122,14 +120,17 @@ struct TreeWork {
     // neighbouring slots, with the row tiles that read the same keys together
     const int R = p.tiles_a_seq, seqs = p.pages.seqs;
     const bool whole = p.budget[1] <= seqs;  // no sequence is split
-    int n[kPlanSeqs / 64];
+    int n[kPlanSeqs / 64], lens[kPlanSeqs / 64];
     int total = 0, slots = seqs, c = 0;
     if (!whole) {
       int most = 1;
 #pragma unroll
       for (int i = 0; i < kPlanSeqs / 64; ++i) {
         const int j = lane + 64 * i;
-        n[i] = j < seqs ? tiles(p, committed(p, j)) : -1;
+        n[i] = -1;
+        if (64 * i >= seqs) continue;
+        lens[i] = committed(p, min(j, seqs - 1));
+        if (j < seqs) n[i] = tiles(p, lens[i]);
         total += max(n[i], 0);
         most = max(most, n[i]);
       }
@@ -138,7 +139,9 @@ struct TreeWork {
       Cut best = cut(n, total, most, seqs, p.budget[0], p.least);
       if (p.budget[1] > p.budget[0]) {
         const Cut more = cut(n, total, most, seqs, p.budget[1], p.least);
-        auto cost = [&](const Cut& x) { return (float)((x.slots * R + 255) / 256) * (p.fixed + (float)x.c * p.tile); };
+        auto cost = [&](const Cut& x) {
+          return (float)((x.slots * R + 255) / 256) * (p.fixed + (float)x.c * p.tile) + (float)x.slots * p.join;
+        };
         if (cost(more) < cost(best)) best = more;
       }
       c = __builtin_amdgcn_readfirstlane(best.c);
@@ -154,11 +157,13 @@ struct TreeWork {
     int split = 0;
     s = slot;
     splits = 1;
+    int len = 0;
     if (!whole) {
       const float inv = 1.f / (float)c;
       int before = 0;
 #pragma unroll
       for (int i = 0; i < kPlanSeqs / 64; ++i) {
+        if (64 * i >= seqs) break;
         const int m = n[i] < 0 ? 0 : max(1, shares(n[i], c, inv));
         const int end = before + wave_inclusive_scan(m);
         const uint64_t here = wave_ballot(slot >= end - m && slot < end);
@@ -166,6 +171,7 @@ struct TreeWork {
           const int l = __builtin_ctzll(here);
           s = 64 * i + l;
           splits = __builtin_amdgcn_readlane(m, l);
+          len = __builtin_amdgcn_readlane(lens[i], l);
           split = slot - (__builtin_amdgcn_readlane(end, l) - splits);
         }
         before = __builtin_amdgcn_readlane(end, 63);
@@ -179,17 +185,23 @@ struct TreeWork {
     s = __builtin_amdgcn_readfirstlane(s);
     splits = __builtin_amdgcn_readfirstlane(splits);
     split = __builtin_amdgcn_readfirstlane(split);
-    const int len = __builtin_amdgcn_readfirstlane(committed(p, s));
+    len = __builtin_amdgcn_readfirstlane(whole ? committed(p, s) : len);
     padded = len < 0;
     prefix = max(len, 0);
     np = (prefix + kAttnTile - 1) / kAttnTile;
     const int t = tiles(p, len), share = (t + splits - 1) / splits;
     cur = split * share;
     tile_end = min(t, cur + share);
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) any |= unit(i).live;
-    if (!any) tile_end = cur;
+    // (a lane a unit, so that the masks are waited for once)
+    const int hc = (p.H + U - 1) / U, node = (r * kUnits + lane) / hc;
+    bool live = lane < kUnits && node < p.N && !padded;
+    if (p.mask && live) {
+      uint64_t any = 0;
+      for (int w = 0; w < p.words; ++w) any |= p.mask[((int64_t)s * p.N + node) * p.words + w];
+      live = any != 0;
+    }
+    alive = (uint32_t)wave_ballot(live);
+    if (!alive) tile_end = cur;
   }
 
   // position of key 64 * ti + lane
@@ -427,15 +439,15 @@ hipError_t launch_tree_lists(const LaunchCtx& cx, const TreeArgs& a, int32_t* li
 static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Rows per workgroup and the budget of splits: the cheapest of four widths, by the
-// costs of the latent kernels (see latent_plan), for sequences that are all as long
-// as the longest. How many splits a sequence gets of the budget is found on the
+// costs of the latent kernels (see latent_plan; 128 rows: of k_latent_pair), for sequences
+// that are all as long as the longest. How many splits a sequence gets of the budget is found on the
 // device, from the lengths.
 TreePlan tree_plan(int seqs, int N, int H, int words, int longest) {
   struct Width {
     int rows, unit;
     double fixed, tile;
   };
-  static const Width widths[] = {{16, 16, 9.0, 1.8}, {32, 16, 11.0, 2.2}, {64, 32, 13.0, 2.25}, {128, 32, 12.0, 3.8}};
+  static const Width widths[] = {{16, 16, 9.0, 1.8}, {32, 16, 11.0, 2.2}, {64, 32, 13.0, 2.25}, {128, 32, 12.0, 3.5}};
   const int tiles = cdiv(longest, kAttnTile) + words;
   TreePlan best{};
   double least = 0.0;
@@ -492,6 +504,7 @@ hipError_t launch_tree(const LaunchCtx& cx, TreeArgs a, const TreePlan& pl, bool
   a.least = pl.least;
   a.fixed = pl.fixed;
   a.tile = pl.tile;
+  a.join = (float)(pl.tiles_a_seq * pl.nq * (kLatent * 4 / 4.8e6));  // (read once more, at the rate of a copy)
   const bool split = pl.budget[1] > seqs;
   if (split) {
     a.rec = static_cast<int32_t*>(ws);
