@@ -332,7 +332,8 @@ struct TreeForm {
 
 // Joins the splits of the sequences that were split (rec says which, and where). As
 // k_join: a workgroup's threads hold COLS of a row's values, SG groups take the
-// splits in turn and are added in a fixed order.
+// splits in turn and are added in a fixed order. Bound by memory where there is much (67 MB
+// in 20.5 us), by latency where there is little (16 rows of 64 splits: 5).
 template <int COLS, int SG>
 __global__ __launch_bounds__(256) void k_tree_join(TreeArgs p, int nq, int unit_rows) {
   constexpr int TPR = COLS / 4, ROWS = 256 / TPR / SG, PARTS = kLatent / COLS;
@@ -387,7 +388,10 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs p, int nq, int unit_
 
 // The rows of the keys of each query: its list's positions (those that are
 // committed), then the nodes of its mask one after the other, then -1. A workgroup
-// takes 1024 entries of one query's list; the one of its end takes the nodes.
+// takes 1024 entries of one query's list; the one of its end takes the nodes. A chain of
+// dependent loads (position, page) that 1024 entries a workgroup cover: 56 queries of 2048, 4.4
+// us, 1.7 of them the launch. (A list of rows lets k_latent_wide walk it as any other: its
+// 40 us would not be shorter for resolving pages itself.)
 constexpr int kListPart = 1024;
 __global__ __launch_bounds__(256) void k_tree_lists(TreeArgs p, int32_t* lists) {
   const int parts = (p.k + kListPart - 1) / kListPart + 1;
