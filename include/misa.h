@@ -56,8 +56,8 @@
  *     workspace `ws` of `ws_bytes` bytes (size it with misa_workspace_bytes,
  *     the attention's with misa_latent_workspace_bytes,
  *     misa_expanded_workspace_bytes and misa_tree_workspace_bytes; 256-byte
- *     alignment is required). Outputs
- *     and workspace must not overlap each other or an input.
+ *     alignment is required). Outputs and workspace must not overlap each other
+ *     or an input.
  *   - `stream` is a hipStream_t (NULL = the legacy default stream). Calls only
  *     enqueue work and return; they never synchronise the host.
  *   - Argument errors are reported synchronously, before anything is enqueued,
@@ -442,7 +442,8 @@ misa_status misa_paged_append(const misa_append_problem* p, void* stream);
  * x and out are [T, H, 64] bf16 bits whose queries and heads are x_t and x_h (out_t
  * and out_h) elements apart (multiples of 8 that are at least 64; 16-byte aligned), so
  * that both may be columns of wider rows. out may be x itself; otherwise they must not
- * overlap. A query whose position lies outside the rotation's is not written. */
+ * overlap. A query whose position lies outside the rotation's is not written. Limits
+ * (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^28. */
 typedef struct misa_rotate_problem {
   int32_t T;
   int32_t H;
@@ -508,7 +509,7 @@ misa_status misa_tree_attention(const misa_tree_problem* p, void* out, float* ls
  * chosen as misa_cache_write chooses a row's; what holds an infinity or NaN gets scale
  * NaN and NaN codes. sum may be residual itself (each value is read before it is
  * written); no other overlap is allowed.
- * Limits (MISA_ERR_UNSUPPORTED past them): width <= 16384, n <= 2^25. */
+ * Limits (MISA_ERR_UNSUPPORTED past them): width <= 16384, n <= 2^25, n * width <= 2^33. */
 typedef struct misa_norm_problem {
   int32_t n;              /* rows (0 is a no-op) */
   int32_t width;          /* a multiple of 8 */

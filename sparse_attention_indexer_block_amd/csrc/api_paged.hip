@@ -7,6 +7,10 @@
 namespace misa {
 
 constexpr int64_t kMaxPositions = (int64_t)1 << 28;  // of one sequence
+// A launch holds fewer than 2^32 threads: eight a rotated row; 64 a normed row of up to 512
+// values (2^25 rows at most), at most one for four values of a wider one.
+constexpr int64_t kMaxTurned = (int64_t)1 << 28;
+constexpr int64_t kMaxValues = (int64_t)1 << 33;
 
 static misa_status check_ld(int64_t ld, int64_t least, const char* name) {
   if (ld < least || ld % 8 != 0)
@@ -122,6 +126,8 @@ misa_status misa_rms_norm(const misa_norm_problem* p, void* y, float* scale, voi
   if (p->n > (1 << 25)) return fail(MISA_ERR_UNSUPPORTED, "n = %d exceeds 2^25 rows", p->n);
   if (p->width < 8 || p->width % 8 != 0) return fail(MISA_ERR_INVALID_ARG, "width = %d must be a multiple of 8", p->width);
   if (p->width > 16384) return fail(MISA_ERR_UNSUPPORTED, "width = %d exceeds 16384", p->width);
+  if ((int64_t)p->n * p->width > kMaxValues)
+    return fail(MISA_ERR_UNSUPPORTED, "n * width = %lld exceeds 2^33 values", (long long)p->n * p->width);
   if (p->dtype != MISA_K_BF16 && p->dtype != MISA_K_FP8_E4M3FN)
     return fail(MISA_ERR_INVALID_ARG, "dtype = %d is not a misa_kdtype", p->dtype);
   const bool fp8 = p->dtype == MISA_K_FP8_E4M3FN;
@@ -157,6 +163,8 @@ misa_status misa_rms_norm(const misa_norm_problem* p, void* y, float* scale, voi
 misa_status misa_rotate(const misa_rotate_problem* p, void* out, int64_t out_t, int64_t out_h, void* stream) {
   if (!p) return fail(MISA_ERR_INVALID_ARG, "problem is NULL");
   MISA_TRY(check_sizes(p->T, p->H, 0.f));
+  if ((int64_t)p->T * p->H > kMaxTurned)
+    return fail(MISA_ERR_UNSUPPORTED, "T * H = %lld exceeds 2^28", (long long)p->T * p->H);
   MISA_TRY(check_rotation(&p->rotation));
   MISA_TRY(check_ld(p->x_h, kRotary, "x_h"));
   MISA_TRY(check_ld(p->x_t, kRotary, "x_t"));

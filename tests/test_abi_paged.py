@@ -126,6 +126,17 @@ def test_norm_checks(kw, status):
     assert S.lib().misa_last_error() != b""
 
 
+def test_calls_past_a_launch_are_refused():
+    # a launch has fewer than 2^32 threads
+    p = _rotate(T=1 << 22, H=65)
+    assert S.lib().misa_rotate(ctypes.byref(p), FAKE, 65 * 64, 64, None) == UNSUPPORTED
+    assert b"2^28" in S.lib().misa_last_error()
+    for n, width in ((1 << 25, 264), ((1 << 19) + 1, 16384), ((1 << 24) + 1, 512)):
+        p = _norm(n=n, width=width, x_ld=width)
+        assert S.lib().misa_rms_norm(ctypes.byref(p), FAKE, FAKE, FAKE, None) == UNSUPPORTED
+        assert b"2^33" in S.lib().misa_last_error()
+
+
 def test_norm_call_checks():
     p = _norm()
     f = lambda y=FAKE, s=FAKE, t=FAKE: S.lib().misa_rms_norm(ctypes.byref(p), y, s, t, None)  # noqa: E731
