@@ -444,14 +444,17 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Rows per workgroup and the budget of splits: the cheapest of four widths, by the
 // costs of the latent kernels (see latent_plan; 128 rows: of k_latent_pair), for sequences
-// that are all as long as the longest. How many splits a sequence gets of the budget is found on the
-// device, from the lengths.
+// that are all as long as the longest. 128 rows of few heads are of several nodes, and the pair
+// kernel takes a word's keys anew for each kind of mask, which it finds by loads one after the
+// other: 7 us each (29 sequences x 41 nodes x 16 heads, 24 keys: 102 us, 51 with 32 rows;
+// 20 x 16 x 3 heads, 700 keys: 59, 41 with 64). How many splits a sequence gets of the budget
+// is found on the device, from the lengths.
 TreePlan tree_plan(int seqs, int N, int H, int words, int longest) {
   struct Width {
     int rows, unit;
-    double fixed, tile;
+    double fixed, tile, kind;
   };
-  static const Width widths[] = {{16, 16, 9.0, 1.8}, {32, 16, 11.0, 2.2}, {64, 32, 13.0, 2.25}, {128, 32, 12.0, 3.5}};
+  static const Width widths[] = {{16, 16, 9.0, 1.8, 0.0}, {32, 16, 11.0, 2.2, 0.0}, {64, 32, 13.0, 2.25, 0.0}, {128, 32, 12.0, 3.5, 7.0}};
   const int tiles = cdiv(longest, kAttnTile) + words;
   TreePlan best{};
   double least = 0.0;
@@ -459,14 +462,16 @@ TreePlan tree_plan(int seqs, int N, int H, int words, int longest) {
     TreePlan pl{};
     pl.nq = w.rows;
     pl.tiles_a_seq = cdiv((int64_t)N * cdiv(H, w.unit), w.rows / w.unit);
-    pl.fixed = (float)w.fixed;
+    const int nodes = std::min(N, std::max(1, w.rows / w.unit / cdiv(H, w.unit)));  // of a row tile
+    const double fixed = w.fixed + (double)(nodes - 1) * words * w.kind;
+    pl.fixed = (float)fixed;
     pl.tile = (float)w.tile;
     const int64_t row_tiles = (int64_t)seqs * pl.tiles_a_seq;
     const int most = seqs > kPlanSeqs ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(256 / row_tiles, tiles));
     for (int want = 1;; want = std::min(2 * want, most)) {
       const int share = cdiv(tiles, want), splits = cdiv(tiles, share);
       const double rounds = (double)((row_tiles * splits + 255) / 256);
-      double cost = rounds * (w.fixed + share * w.tile);
+      double cost = rounds * (fixed + share * w.tile);
       if (splits > 1) cost += 3.5 + 0.05 * splits + (double)splits * seqs * N * H * (kLatent * 4) / 2.3e6;
       if (best.nq == 0 || cost < least) {
         least = cost;

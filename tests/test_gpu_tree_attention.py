@@ -40,8 +40,8 @@ def _some(S_, N, count=8):
 CUTS = [  # sequences, nodes, heads, longest prefix, the cut
     (2, 1, 3, 50, (16, False)), (2, 1, 3, 600, (16, True)), (3, 5, 16, 50, (16, False)), (300, 2, 16, 100, (32, False)),
     (9, 17, 3, 700, (32, True)), (70, 3, 33, 30, (64, False)), (40, 6, 20, 1000, (64, True)), (300, 2, 128, 100, (128, False)),
-    (20, 16, 3, 700, (128, True)), (4, 7, 128, 500, (16, False)), (3, 40, 40, 300, (32, False)),
-    (24, 4, 128, 2000, (64, True))]
+    (20, 16, 3, 700, (32, False)), (4, 7, 128, 500, (16, False)), (3, 40, 40, 300, (32, False)),
+    (24, 4, 128, 2000, (64, True)), (40, 16, 3, 1000, (128, True))]  # (the last: rows of four nodes share a workgroup)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
