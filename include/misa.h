@@ -503,7 +503,8 @@ misa_status misa_tree_attention(const misa_tree_problem* p, void* out, float* ls
  * Root-mean-square norm of n rows, with a residual added before it:
  *   h = x + residual (x without one),  sum = h,  y = h / sqrt(mean(h^2) + eps) * weight
  * h and y are formed in fp32 (a sum past its range is infinite), the mean square in
- * fp64, and each result is rounded once. dtype MISA_K_BF16: y is [n, width] bf16 bits.
+ * fp64, its reciprocal root in fp32 (infinite where mean(h^2) + eps is below 2^-256),
+ * and each result is rounded once. dtype MISA_K_BF16: y is [n, width] bf16 bits.
  * MISA_K_FP8_E4M3FN: y is [n, width] codes with y = code * scale, scale [n] for the row
  * (group 0) or [n, ceil(width / 128)] for each 128 columns (group 128), a power of two
  * chosen as misa_cache_write chooses a row's; what holds an infinity or NaN gets scale
