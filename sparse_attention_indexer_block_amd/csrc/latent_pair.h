@@ -403,7 +403,9 @@ __global__ __launch_bounds__(256, 1) void k_latent_pair(typename Form::Args p) {
     const uint32_t seen = (uint32_t)(cur.held >> (32 * N)) & cur.own;
     has |= cur.own;
     if (__builtin_expect(seen != 0xffffffffu, 0)) {
-      const uint32_t bits = seen >> anew(4 * h2);  // (not sixteen masks kept in registers)
+      // (not sixteen masks kept in registers; with codes not the lane's half either: it was spilled,
+      // and its reload waited for the copies in flight)
+      const uint32_t bits = seen >> (FP8 ? (__builtin_amdgcn_mbcnt_lo(~0u, anew(0u)) >> 5) * 4 : (uint32_t)anew(4 * h2));
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? s[e] : -INFINITY;
     }
