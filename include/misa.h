@@ -479,7 +479,7 @@ typedef struct misa_tree_problem {
   int32_t N;              /* nodes a sequence, >= 1 */
   int32_t H;              /* heads, >= 1 */
   int32_t k;              /* entries of a query's list (idx), or 0 */
-  int32_t words;          /* 64-bit words of a mask, or 0 */
+  int32_t words;          /* 64-bit words of a mask, >= ceil(N / 64), or 0 */
   float sm_scale;         /* as in misa_latent_problem */
   int32_t longest;        /* >= 0 */
   const void* q;          /* [seqs,N,H,576] bf16 bits, 16-byte aligned */

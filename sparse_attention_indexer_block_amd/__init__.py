@@ -665,8 +665,8 @@ def tree_attention(q, prefix, table, page, C, sm_scale, c_scale=None, rope=None,
     prefix[s] int32 committed tokens of its sequence, or those of them that idx
     [S, N, k] int32 names (positions, -1: none), and of the drafted ones, which
     follow at positions prefix[s] + b, those whose bit b its mask has: int64 [S, N]
-    or [S, N, words], itself and its ancestors; without masks itself and those
-    before it. A mask of 0 (or a prefix below 0) marks padding: zeros, -inf.
+    (N up to 64) or [S, N, words >= N / 64], itself and its ancestors; without masks
+    itself and those before it. A mask of 0 (or a prefix below 0) marks padding: zeros, -inf.
     longest: the length that the call is planned for (results do not depend on
     it). The result carries no gradient (it is detached from q and the cache)."""
     p = make_tree_problem(q, prefix, table, page, C, sm_scale, c_scale, rope, mask, idx, longest)

@@ -84,6 +84,8 @@ static misa_status check_tree(const misa_tree_problem* p) {
   if (some && (p->mask ? p->words < 1 : p->words != 0))
     return fail(MISA_ERR_INVALID_ARG, "words = %d must be >= 1 with mask and 0 without", p->words);
   if (p->words > 1024) return fail(MISA_ERR_UNSUPPORTED, "words = %d exceeds 1024", p->words);
+  if (some && p->mask && p->words < (p->N + 63) / 64)  // (a node past the last word could not name itself)
+    return fail(MISA_ERR_INVALID_ARG, "words = %d must be >= %d for %d nodes", p->words, (p->N + 63) / 64, p->N);
   if (some && (p->idx ? p->k < 1 : p->k != 0))
     return fail(MISA_ERR_INVALID_ARG, "k = %d must be >= 1 with idx and 0 without", p->k);
   if (p->k > (1 << 24)) return fail(MISA_ERR_UNSUPPORTED, "k = %d exceeds 2^24", p->k);
