@@ -419,6 +419,13 @@ def _first(t, name: str, dtypes, dims: int):
     return shape, t.get_device()
 
 
+def _int32(n: int, name: str) -> int:
+    """n, which a C structure takes modulo 2^32, if that changes nothing."""
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} = {n} does not fit in 32 bits")
+    return n
+
+
 def _on(dev: int, call, *args):
     """call(*args, current stream of GPU dev) with dev as the current GPU."""
     if torch._C._cuda_getDevice() == dev:  # (a tensor of GPU dev exists: the GPUs are initialised)
@@ -501,7 +508,7 @@ def make_latent_problem(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=N
     (_, k), _ = _first(idx, "idx", _I32, 2)
     if k < 1:
         raise ValueError("idx must have at least one column")
-    return LatentProblem(T, H, k, sm_scale, at, _arg(idx, "idx", _I32, (T, k), dev), None, first, c)
+    return LatentProblem(T, H, _int32(k, "idx's columns"), sm_scale, at, _arg(idx, "idx", _I32, (T, k), dev), None, first, c)
 
 
 def latent_attention(q, C, sm_scale, pos=None, idx=None, c_scale=None, rope=None, base=None, with_lse=False,
@@ -548,7 +555,7 @@ _I64, _WEIGHT = (torch.int64,), (torch.bfloat16, torch.int16, torch.float32)
 
 def _pages(table, page, dev) -> Pages:
     seqs, per = table.shape if table is not None and table.dim() == 2 else _first(table, "table", _I32, 2)[0]
-    return Pages(_arg(table, "table", _I32, (seqs, per), dev), seqs, per, page)
+    return Pages(_arg(table, "table", _I32, (seqs, per), dev), seqs, _int32(per, "table's pages"), _int32(page, "page"))
 
 
 def _weight(weight, width, dev):
@@ -596,6 +603,7 @@ def paged_append(x, seq, pos, table, page, C, c_scale=None, rope=None, weight=No
         turning = _rotation(rot, pairs, dev)
         if rot_at is None:
             rot_at = d if dr else 0
+        _int32(rot_at, "rot_at")
     elif rot_at is not None or pairs:
         raise ValueError("rot_at and pairs are only for a rotation (rot)")
     else:
@@ -637,7 +645,7 @@ def rotate(x, pos, rot, pairs=False, out=None):
 def make_tree_problem(q, prefix, table, page, C, sm_scale, c_scale=None, rope=None, mask=None, idx=None, longest=0) -> TreeProblem:
     c = make_cache(C, c_scale, rope)
     (S, N, H, _), dev = _first(q, "q", _BF16, 4)
-    p = TreeProblem(N, H, 0, 0, sm_scale, longest, _arg(q, "q", _BF16, (S, N, H, LATENT + ROTARY), C.get_device()),
+    p = TreeProblem(N, H, 0, 0, sm_scale, _int32(longest, "longest"), _arg(q, "q", _BF16, (S, N, H, LATENT + ROTARY), C.get_device()),
                     _arg(prefix, "prefix", _I32, (S,), dev), None, None, _pages(table, page, dev), c)
     if p.pages.seqs != S:
         raise ValueError(f"table has {p.pages.seqs} sequences, not {S}")
@@ -645,13 +653,13 @@ def make_tree_problem(q, prefix, table, page, C, sm_scale, c_scale=None, rope=No
         if mask.dim() == 2:
             p.mask, p.words = _arg(mask, "mask", _I64, (S, N), dev), 1
         else:
-            (_, _, p.words), _ = _first(mask, "mask", _I64, 3)
-            p.mask = _arg(mask, "mask", _I64, (S, N, p.words), dev)
+            (_, _, words), _ = _first(mask, "mask", _I64, 3)
+            p.mask, p.words = _arg(mask, "mask", _I64, (S, N, words), dev), _int32(words, "mask's words")
         if p.words < 1:
             raise ValueError("mask must have at least one word")
     if idx is not None:
-        (_, _, p.k), _ = _first(idx, "idx", _I32, 3)
-        p.idx = _arg(idx, "idx", _I32, (S, N, p.k), dev)
+        (_, _, k), _ = _first(idx, "idx", _I32, 3)
+        p.idx, p.k = _arg(idx, "idx", _I32, (S, N, k), dev), _int32(k, "idx's columns")
         if p.k < 1:
             raise ValueError("idx must have at least one column")
     return p
@@ -686,7 +694,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, coded=False, group=0, out=None,
     at, n, ld = _rows(x, "x", width, dev)
     w_at, w_dtype = _weight(weight, width, dev)
     shape = (n, width)
-    p = NormProblem(n, width, at, ld, None, w_at, w_dtype, 1 if coded else 0, group, eps)
+    p = NormProblem(_int32(n, "x's rows"), _int32(width, "x's width"), at, ld, None, w_at, w_dtype, 1 if coded else 0, group, eps)
     t_at = s_at = None
     if residual is not None:
         p.residual = _arg(residual, "residual", _BF16, shape, dev)
