@@ -11,8 +11,8 @@ namespace misa {
 
 // W waves a row, CH chunks of eight values a lane (chunk = thread + 64 W i); a
 // workgroup of four waves takes 4 / W rows, or one of more waves. A row is read once
-// and stays in registers; the squares are summed in fp64, exact enough that the scales of
-// codes do not depend on the order. Bound by memory: 16,384 rows of 4096 with residual, to
+// and stays in registers; the squares are summed in fp64, so that the root, and the scales of
+// codes with it, depend on the order only next to a rounding border (see squares). Bound by memory: 16,384 rows of 4096 with residual, to
 // codes with a scale for 128 columns, 472 MB in 84 us, 5.6 TB/s (a plain copy, which writes
 // as much as it reads, 4.9); eight rows 3.7 us, of which 1.7 are the launch and the rest the
 // loads and two barriers one after the other.

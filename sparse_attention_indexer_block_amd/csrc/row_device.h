@@ -68,8 +68,10 @@ __device__ __forceinline__ void load_weights(const void* weight, bool f32, int a
 }
 
 // The sum of squares of a row is held in 64 bits: a square of an fp32 value is exact
-// there, so the reciprocal root comes out the same whatever the order of the sum,
-// and no magnitude overflows.
+// there and no magnitude overflows. Each addition rounds (2^-53), up to 38 of them one
+// after the other (a lane's values, then lanes, then waves), so the sum is off by less
+// than 2^-47 of itself in whatever order, and another order gives another fp32 root only
+// where the root lies within 2^-47 of itself from a border of fp32's rounding.
 __device__ __forceinline__ double squares(const float (&x)[8], double sum) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum = fma((double)x[i], (double)x[i], sum);
