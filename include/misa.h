@@ -416,6 +416,9 @@ typedef enum misa_wdtype {
  *   3. coded, if the cache holds codes, as misa_cache_write does, with the scale that
  *      the values of steps 1 and 2 call for.
  * Steps 1 and 2 are formed in fp32, and a value is rounded once, as it is stored.
+ * The selections read a sequence's keys as a flat K[L,128]: indexer keys are selected from
+ * where the pages of their sequence lie one after the other, and misa_cache_read reads them
+ * from any pages.
  * A row whose seq lies outside [0, seqs), whose pos outside [0, per * page), whose
  * turn outside the rotation's positions (if it is rotated) or whose page is none
  * writes nothing. Rows must name distinct places: one named twice holds either row's
@@ -471,7 +474,9 @@ misa_status misa_rotate(const misa_rotate_problem* p, void* out, int64_t out_t, 
  * no effect on it. Sequences may differ in length; the call is planned for a longest
  * prefix of `longest` (0: per * page), which may be exceeded: it decides how the call
  * is cut and never what it returns, to within rounding. Results do not depend on what
- * else runs, and the same call gives the same bits.
+ * else runs, and the same call gives the same bits. The keys of up to 256 sequences are
+ * split over the card by the sequences' lengths; past 256 every sequence is worked
+ * whole, and a batch takes less time in several calls.
  * Limits (MISA_ERR_UNSUPPORTED past them): N <= 2^16, words <= 1024, seqs * N <= 2^22,
  * seqs * N * H <= 2^30, k <= 2^24, seqs * N * (k + 64 words) <= 2^31 with idx (words =
  * ceil(N / 64) where mask is NULL). */

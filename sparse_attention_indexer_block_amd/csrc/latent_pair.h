@@ -90,9 +90,10 @@ struct PairLds {
 //   - the next step's scores run beside this one's softmax, the copies three steps ahead
 //     beside the values' products, the reads of LDS ahead of both.
 // A second wave a SIMD to issue beside does not fit: 256 sums and 144 of queries a lane.
-// 2 sequences x 64 tokens x 128 heads over 32,000 keys, bf16: 893 us, 1.28 PFLOP/s (a
+// 2 sequences x 64 tokens x 128 heads over 32,000 keys, bf16: 936 us in the median of the first
+// thirty calls of a process, 1.22 PFLOP/s, and 893 under a longer load (a
 // library's product of 8192^3 reaches 1.32, and the clock falls as the kernel gains: the
-// last step took 9 % of its cycles and 2.4 % of its time); k_latent_wide 1060. A step of 32
+// last step took 9 % of its cycles and 2.4 % of its time); k_latent_wide 1060 under that load. A step of 32
 // keys: 70 cycles until the scores, 1670 with them, 1670 of values. With codes 85, 2550 and
 // 1860: the issue of 192 conversions bounds the scores. A workgroup's rest, some 45,000
 // cycles: 10,000 to find its share, 9,000 for the queries, 9,000 until the first scores are

@@ -15,6 +15,9 @@
 namespace misa {
 
 // The largest batch whose keys are split: one lane of a wave holds kPlanSeqs / 64 sequences.
+// Past it a sequence's row tiles are whole: one token of 16 heads over 8000 coded keys each
+// takes 323 us with 256 sequences and 607 with 257 (of 200 to 2000 keys beside one of 8000:
+// 103 and 275), 128 sequences 183.
 constexpr int kPlanSeqs = 256;
 
 // The walk of a workgroup: a row tile of one sequence (units of U heads of one node)
@@ -448,7 +451,9 @@ static int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // that are all as long as the longest. 128 rows of few heads are of several nodes, and the pair
 // kernel takes a word's keys anew for each kind of mask, which it finds by loads one after the
 // other: 7 us each (29 sequences x 41 nodes x 16 heads, 24 keys: 102 us, 51 with 32 rows;
-// 20 x 16 x 3 heads, 700 keys: 59, 41 with 64). How many splits a sequence gets of the budget
+// 20 x 16 x 3 heads, 700 keys: 59, 41 with 64). That is charged to every workgroup, though with
+// split keys only the last splits of a sequence meet words: such calls may be given a narrower
+// width than the fastest. How many splits a sequence gets of the budget
 // is found on the device, from the lengths.
 TreePlan tree_plan(int seqs, int N, int H, int words, int longest) {
   struct Width {
