@@ -445,8 +445,9 @@ misa_status misa_paged_append(const misa_append_problem* p, void* stream);
  * x and out are [T, H, 64] bf16 bits whose queries and heads are x_t and x_h (out_t
  * and out_h) elements apart (multiples of 8 that are at least 64; 16-byte aligned), so
  * that both may be columns of wider rows; no two rows of out may overlap. out may be x
- * itself, with its distances; otherwise they must not overlap. A query whose position lies outside the rotation's is not written. Limits
- * (MISA_ERR_UNSUPPORTED past them): T <= 2^22, T * H <= 2^28. */
+ * itself, with its distances; otherwise they must not overlap. A query whose position
+ * lies outside the rotation's is not written. Limits (MISA_ERR_UNSUPPORTED past them):
+ * T <= 2^22, T * H <= 2^28. */
 typedef struct misa_rotate_problem {
   int32_t T;
   int32_t H;
