@@ -1,5 +1,6 @@
 """Refused calls of the paged caches, the rotation, the norm and the attention of drafted
 tokens leave their outputs as they were."""
+import numpy as np
 import pytest
 import torch
 
