@@ -477,7 +477,7 @@ misa_status misa_rotate(const misa_rotate_problem* p, void* out, int64_t out_t, 
  * is cut and never what it returns, to within rounding. Results do not depend on what
  * else runs, and the same call gives the same bits. The keys of up to 256 sequences are
  * split over the card by the sequences' lengths; past 256 every sequence is worked
- * whole, and a batch takes less time in several calls.
+ * whole, and a batch of few more, or of very unequal lengths, takes less time in two calls.
  * Limits (MISA_ERR_UNSUPPORTED past them): N <= 2^16, words <= 1024, seqs * N <= 2^22,
  * seqs * N * H <= 2^30, k <= 2^24, seqs * N * (k + 64 words) <= 2^31 with idx (words =
  * ceil(N / 64) where mask is NULL). */
